@@ -7,6 +7,11 @@ pointers and the current HIP stream. All arithmetic runs in libsharq.so.
     prep = prepare(x, gamma=None, n=2, m=4)        # x: bf16 [T, K] on the GPU
     wq = quantize_mxfp4(w)                         # w: bf16 [O, K]
     y = linear(prep, wq)                           # fp32 [T, O]
+
+The plain MXFP4 path (one operand, no decomposition) and expert routing:
+
+    y = linear_mxfp4(quantize_mxfp4(x), wq)        # fp32 or bf16 [T, O]
+    r = moe_route(logits, k)                       # experts, weights, dispatch plan
 """
 
 from __future__ import annotations
@@ -40,6 +45,12 @@ __all__ = [
     "pack_mxfp4",
     "pack_nvfp4",
     "unpack_stage_major",
+    "linear_mxfp4",
+    "linear_silu_mxfp4",
+    "linear_grouped_mxfp4",
+    "linear_grouped_silu_mxfp4",
+    "Routing",
+    "moe_route",
     "SharqError",
     "status_string",
 ]
@@ -98,6 +109,23 @@ def _need(t, dtype, name, ndim=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims")
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+
+
+def _run(name, device, *args):
+    """Enqueue an entry point on the device's current stream and raise on a bad status."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = _lib.call(name, *args, _stream(device))
+    else:
+        st = _lib.call(name, *args, _stream(device))
+    _lib.check(name, st)
 
 
 def _check_stage_major(codes, scales, R, K, name):
@@ -177,12 +205,18 @@ def prepare(x, gamma=None, n: int = 2, m: int = 4, with_mask: bool = True, out: 
     return out
 
 
-def quantize_mxfp4(x, out: Optional[MXFP4] = None) -> MXFP4:
+def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional[float] = None) -> MXFP4:
     """Plain MXFP4 along the last axis of a bf16 [R, K] tensor (e.g. a weight
     [O, K]), or of a stack of expert weights [E, O, K] (one call per expert,
-    so each expert owns a contiguous [G, O, 4] scale block)."""
+    so each expert owns a contiguous [G, O, 4] scale block). With rms_eps the
+    rows of a [R, K] tensor are RMS-normed first (per-row 1/rms, then gamma
+    when given), as prepare(rms_eps=...) norms them."""
     torch = _torch()
+    if gamma is not None and rms_eps is None:
+        raise ValueError("gamma is the weight of the norm: it needs rms_eps")
     if x.dim() == 3:
+        if rms_eps is not None:
+            raise ValueError("the norm is for [R, K] activations")
         E, R, K = x.shape
         if out is None:
             out = MXFP4(torch.empty((E, stages(K), R, 64), dtype=torch.uint8, device=x.device),
@@ -200,6 +234,16 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None) -> MXFP4:
     _need(out.codes, torch.uint8, "out.codes", 3)
     _need(out.scales, torch.uint8, "out.scales", 3)
     _check_stage_major(out.codes, out.scales, R, K, "out")
+    if rms_eps is not None:
+        if gamma is not None:
+            _need(gamma, torch.bfloat16, "gamma", 1)
+            if gamma.numel() != K:  # the kernels read K entries of gamma
+                raise ValueError(f"gamma must hold K = {K} entries, got {gamma.numel()}")
+            gamma = gamma.contiguous()
+        _same_device(x, gamma, out.codes, out.scales)
+        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, x.stride(0), _ptr(gamma), float(rms_eps), 0,
+             out.codes.data_ptr(), out.scales.data_ptr())
+        return out
     st = _lib.call("sharq_quantize_mxfp4", x.data_ptr(), R, K, x.stride(0), out.codes.data_ptr(),
                    out.scales.data_ptr(), _stream(x.device))
     _lib.check("sharq_quantize_mxfp4", st)
@@ -474,9 +518,11 @@ def expand_backbone(cb: CompactBackbone, bb_codes=None, mask=None, with_mask: bo
 
 def moe_combine(y, pair_index, weights, out=None, bf16: bool = False):
     """out[t] = sum_j weights[t, j] * y[pair_index[t, j]] (slots with -1 skipped),
-    fp32 accumulation in slot order; fp32 [T, H] or, with bf16, bf16 [T, H]."""
+    fp32 accumulation in slot order; fp32 [T, H] or, with bf16, bf16 [T, H].
+    y is fp32 or bf16."""
     torch = _torch()
-    _need(y, torch.float32, "y", 2)
+    rows_bf16 = isinstance(y, torch.Tensor) and y.dtype == torch.bfloat16
+    _need(y, torch.bfloat16 if rows_bf16 else torch.float32, "y", 2)
     _need(pair_index, torch.int32, "pair_index", 2)
     _need(weights, torch.float32, "weights", 2)
     if not (y.is_contiguous() and pair_index.is_contiguous() and weights.is_contiguous()):
@@ -489,6 +535,11 @@ def moe_combine(y, pair_index, weights, out=None, bf16: bool = False):
     if out is None:
         out = torch.empty((T, H), dtype=dt, device=y.device)
     _check_matrix(out, dt, T, H, "out", contiguous=True)
+    if rows_bf16:
+        _same_device(y, pair_index, weights, out)
+        _run("sharq_moe_combine_bf16", y.device, y.data_ptr(), P, H, pair_index.data_ptr(), weights.data_ptr(), T, k,
+             0 if bf16 else out.data_ptr(), out.data_ptr() if bf16 else 0)
+        return out
     st = _lib.call("sharq_moe_combine", y.data_ptr(), P, H, pair_index.data_ptr(), weights.data_ptr(), T, k,
                    0 if bf16 else out.data_ptr(), out.data_ptr() if bf16 else 0, _stream(y.device))
     _lib.check("sharq_moe_combine", st)
@@ -678,3 +729,223 @@ def unpack_stage_major(codes, scales, K: int):
                    codes_rm.data_ptr(), scales_rm.data_ptr(), _stream(codes.device))
     _lib.check("sharq_unpack_stage_major", st)
     return codes_rm, scales_rm
+
+
+# ---------------------------------------------------------------------------
+# Plain MXFP4 path: one activation operand, no decomposition
+# ---------------------------------------------------------------------------
+
+
+def _check_mx(t, name, ndim=3):
+    """An MXFP4 tensor's codes and scales are contiguous, stage-major and fit its K."""
+    torch = _torch()
+    _need(t.codes, torch.uint8, name + ".codes", ndim)
+    _need(t.scales, torch.uint8, name + ".scales", ndim)
+    lead = tuple(t.codes.shape[:-1])
+    if lead[-2] != stages(t.K) or t.codes.shape[-1] != 64 or tuple(t.scales.shape) != lead + (4,):
+        raise ValueError(f"{name}: expected stage-major codes [.., {stages(t.K)}, R, 64] and scales "
+                         f"[.., {stages(t.K)}, R, 4], got {tuple(t.codes.shape)} and {tuple(t.scales.shape)}")
+    if not (t.codes.is_contiguous() and t.scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous")
+
+
+def _out_dtype(out, dtype):
+    """The type of a product's output and its number in the ABI."""
+    torch = _torch()
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype asks for {dtype}")
+    dtype = out.dtype if out is not None else dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"the output is float32 or bfloat16, not {dtype}")
+    return dtype, 0 if dtype == torch.float32 else 1
+
+
+def _scratch(device, nbytes):
+    """Workspace of one call, from the allocator that orders it with the
+    stream's work (in a graph, from the graph's own memory); None for 0."""
+    torch = _torch()
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
+
+
+def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True):
+    """One plain MXFP4 product Y = deq(a) deq(w)^T, [T, O] of dtype float32
+    (the default) or bfloat16 (the fp32 sum rounded once). With split_k, K is
+    split over a workspace where the library expects that to be faster (single
+    tokens, few output tiles); the result is deterministic either way."""
+    torch = _torch()
+    _check_mx(a, "a")
+    _check_mx(w, "w")
+    if w.K != a.K:
+        raise ValueError("weight K does not match the activation K")
+    T, O, K = a.codes.shape[1], w.codes.shape[1], a.K
+    dtype, number = _out_dtype(out, dtype)
+    dev = a.codes.device
+    if out is None:
+        out = torch.empty((T, O), dtype=dtype, device=dev)
+    _check_matrix(out, dtype, T, O, "out")
+    _same_device(a.codes, a.scales, w.codes, w.scales, out)
+    ws = _scratch(dev, _lib.call("sharq_linear_mxfp4_workspace_bytes", T, O, K) if split_k else 0)
+    _run("sharq_linear_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+         T, O, K, out.data_ptr(), max(out.stride(0), O), number, _ptr(ws), 0 if ws is None else ws.numel())
+    return out
+
+
+def _mx_like(rows, K, device):
+    torch = _torch()
+    return MXFP4(torch.empty((stages(K), rows, 64), dtype=torch.uint8, device=device),
+                 torch.empty((stages(K), rows, 4), dtype=torch.uint8, device=device), K)
+
+
+def linear_silu_mxfp4(a: MXFP4, w_gu: MXFP4, out: Optional[MXFP4] = None, split_k: bool = True) -> MXFP4:
+    """Fused gate|up projection on the plain path: the product with w_gu (I
+    gate rows, then I up rows), h = bf16(silu(gate) * up), MXFP4 of h. Equals
+    linear_mxfp4(split_k) -> silu_mul -> quantize_mxfp4 bit for bit; neither
+    the product nor h passes through memory (but for the fp32 partials of a
+    split K)."""
+    _check_mx(a, "a")
+    _check_mx(w_gu, "w_gu")
+    if w_gu.K != a.K or w_gu.codes.shape[1] % 2:
+        raise ValueError("w_gu must be [2I, K] with the activation's K")
+    T, I, K = a.codes.shape[1], w_gu.codes.shape[1] // 2, a.K
+    dev = a.codes.device
+    if out is None:
+        out = _mx_like(T, I, dev)
+    else:
+        _check_mx(out, "out")
+        if out.K != I or out.codes.shape[1] != T:
+            raise ValueError(f"out must be an MXFP4 tensor of [{T}, {I}]")
+    _same_device(a.codes, a.scales, w_gu.codes, w_gu.scales, out.codes, out.scales)
+    ws = _scratch(dev, _lib.call("sharq_linear_silu_mxfp4_workspace_bytes", T, I, K) if split_k else 0)
+    _run("sharq_linear_silu_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w_gu.codes.data_ptr(),
+         w_gu.scales.data_ptr(), T, I, K, out.codes.data_ptr(), out.scales.data_ptr(), _ptr(ws),
+         0 if ws is None else ws.numel())
+    return out
+
+
+def _check_grouped(a, w, seg_offsets, a_rows, name):
+    """(T_src, E, rows of the weight, P) of a grouped call on the plain path."""
+    torch = _torch()
+    _check_mx(a, "a")
+    _check_mx(w, name, 4)
+    if w.K != a.K:
+        raise ValueError("weight K does not match the activation K")
+    E = w.codes.shape[0]
+    _need(seg_offsets, torch.int32, "seg_offsets", 1)
+    if seg_offsets.numel() != E + 1 or not seg_offsets.is_contiguous():
+        raise ValueError("seg_offsets must be a contiguous [E + 1] tensor")
+    if a_rows is not None:
+        _need(a_rows, torch.int32, "a_rows", 1)
+        if not a_rows.is_contiguous():
+            raise ValueError("a_rows must be contiguous")
+    _same_device(a.codes, a.scales, w.codes, w.scales, seg_offsets, a_rows)
+    T = a.codes.shape[1]
+    return T, E, w.codes.shape[2], T if a_rows is None else a_rows.numel()
+
+
+def linear_grouped_mxfp4(a: MXFP4, w: MXFP4, seg_offsets, a_rows=None, out=None, dtype=None):
+    """linear_mxfp4 per expert segment: row p of the [P, O] result (float32 or
+    bfloat16) is activation row a_rows[p] (row p without a_rows) times the
+    weight of the expert e with seg_offsets[e] <= p < seg_offsets[e + 1].
+    w.codes is [E, G, O, 64]. Rows behind the last segment are not written."""
+    torch = _torch()
+    T, E, O, P = _check_grouped(a, w, seg_offsets, a_rows, "w")
+    dtype, number = _out_dtype(out, dtype)
+    if out is None:
+        out = torch.empty((P, O), dtype=dtype, device=a.codes.device)
+    _check_matrix(out, dtype, P, O, "out", contiguous=True)
+    _same_device(a.codes, out)
+    _run("sharq_linear_grouped_mxfp4", a.codes.device, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w.codes.data_ptr(), w.scales.data_ptr(), P, O, a.K, out.data_ptr(), number)
+    return out
+
+
+def linear_grouped_silu_mxfp4(a: MXFP4, w_gu: MXFP4, seg_offsets, a_rows=None,
+                              out: Optional[MXFP4] = None) -> MXFP4:
+    """linear_silu_mxfp4 per expert segment: MXFP4 of h [P, I] for expert
+    weights w_gu.codes [E, G, 2I, 64]. Rows behind the last segment are not
+    written."""
+    T, E, O, P = _check_grouped(a, w_gu, seg_offsets, a_rows, "w_gu")
+    if O % 2:
+        raise ValueError("w_gu must be [E, 2I, K]")
+    if out is None:
+        out = _mx_like(P, O // 2, a.codes.device)
+    else:
+        _check_mx(out, "out")
+        if out.K != O // 2 or out.codes.shape[1] != P:
+            raise ValueError(f"out must be an MXFP4 tensor of [{P}, {O // 2}]")
+        _same_device(a.codes, out.codes, out.scales)
+    _run("sharq_linear_grouped_silu_mxfp4", a.codes.device, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), P, O // 2, a.K,
+         out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Expert routing
+# ---------------------------------------------------------------------------
+
+
+class Routing(NamedTuple):
+    """Where each token goes: the chosen experts and their weights (best
+    first), and the pairs (token, expert) sorted by expert, as the grouped
+    calls and moe_combine read them."""
+    expert: "object"       # i32 [T, k], -1 in an empty slot
+    weight: "object"       # fp32 [T, k], 0 in an empty slot
+    seg_offsets: "object"  # i32 [E + 1]
+    a_rows: "object"       # i32 [T * k], -1 behind the last pair
+    pair_index: "object"   # i32 [T, k], -1 in an empty slot
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "sum2": 1}
+
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: Optional[int] = None,
+              group_score: str = "max", renormalize: bool = True, scale: float = 1.0, num_tokens=None) -> Routing:
+    """The k experts of each token from router logits [T, E] (float32, bfloat16
+    or float16; rows may be strided), their weights and the dispatch plan.
+
+    Experts are ordered by their logit, or with bias (fp32 [E]) by score +
+    bias; equal ones go to the lower index, and an expert whose logit is -inf
+    or NaN is never chosen (slots that stay empty hold -1 and weight 0). With
+    groups > 1 only the top_groups best groups of consecutive experts take
+    part, judged by their largest value ("max") or the sum of their two largest
+    scores + bias ("sum2"). weight is the score without the bias, divided by
+    the sum over the chosen with renormalize, times scale. Rows from
+    num_tokens (int32 [1] on the device) on are padding and choose nothing."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if logits.dtype not in kinds:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _need(logits, logits.dtype, "logits", 2)
+    T, E = logits.shape
+    if T and (logits.stride(1) != 1 and E > 1):
+        raise ValueError("logits rows must be contiguous along the experts")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.numel() != E or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous [{E}] tensor")
+    if num_tokens is not None:
+        _need(num_tokens, torch.int32, "num_tokens")
+        if num_tokens.numel() != 1:
+            raise ValueError("num_tokens must hold one value")
+    _same_device(logits, bias, num_tokens)
+    dev = logits.device
+    r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
+                torch.empty((T, k), dtype=torch.float32, device=dev),
+                torch.empty(E + 1, dtype=torch.int32, device=dev),
+                torch.empty(T * k, dtype=torch.int32, device=dev),
+                torch.empty((T, k), dtype=torch.int32, device=dev))
+    ws = _scratch(dev, _lib.call("sharq_moe_route_workspace_bytes", T, E))
+    _run("sharq_moe_route", dev, logits.data_ptr(), kinds[logits.dtype], T, E,
+         logits.stride(0) if T > 1 else E, _ptr(bias), k, _SCORES[score], groups,
+         groups if top_groups is None else top_groups, _GROUP_SCORES[group_score], int(renormalize), float(scale),
+         _ptr(num_tokens), r.expert.data_ptr(), r.weight.data_ptr(), r.seg_offsets.data_ptr(), r.a_rows.data_ptr(),
+         r.pair_index.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
+    return r

@@ -56,6 +56,19 @@ SIGNATURES = {
     "sharq_compress_backbone": (_INT, [_P, _P, _I64, _I64, _INT, _INT, _P, _P, _P]),
     "sharq_expand_backbone": (_INT, [_P, _P, _I64, _I64, _INT, _INT, _P, _P, _P]),
     "sharq_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, ctypes.c_int32, _P, _P, _P]),
+    "sharq_quantize_mxfp4_rms": (_INT, [_P, _I64, _I64, _I64, _P, ctypes.c_float, _P, _P, _P, _P]),
+    "sharq_linear_mxfp4_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "sharq_linear_mxfp4": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _INT, _P, _I64, _P]),
+    "sharq_linear_silu_mxfp4_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "sharq_linear_silu_mxfp4": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P]),
+    "sharq_linear_grouped_mxfp4": (_INT, [_P, _P, _I64, _P, _P, ctypes.c_int32, _P, _P, _I64, _I64, _I64, _P, _INT,
+                                          _P]),
+    "sharq_linear_grouped_silu_mxfp4": (_INT, [_P, _P, _I64, _P, _P, ctypes.c_int32, _P, _P, _I64, _I64, _I64, _P,
+                                               _P, _P]),
+    "sharq_moe_route_workspace_bytes": (_I64, [_I64, ctypes.c_int32]),
+    "sharq_moe_route": (_INT, [_P, _INT, _I64, ctypes.c_int32, _I64, _P, ctypes.c_int32, _INT, ctypes.c_int32,
+                               ctypes.c_int32, _INT, _INT, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "sharq_moe_combine_bf16": (_INT, [_P, _I64, _I64, _P, _P, _I64, ctypes.c_int32, _P, _P, _P]),
     "sharq_silu_mul": (_INT, [_P, _I64, _I64, _P, _P]),
 }
 

@@ -112,7 +112,80 @@ __global__ __launch_bounds__(256) void moe_combine_batched_kernel(const float* _
   combine_store(acc, t, c, H, out, out_bf16);
 }
 
+// The combine of bf16 rows: the same sum, a lane owns kCols columns (8: one
+// 16-byte read a slot; 4 where a row is no multiple of 16 bytes). The indices
+// and rows of kBatch slots are in flight together.
+template <int kCols>
+__global__ __launch_bounds__(256) void moe_combine_bf16_kernel(const uint16_t* __restrict__ y, int64_t P, int64_t H,
+                                                               const int32_t* __restrict__ pair_index,
+                                                               const float* __restrict__ weights, int k,
+                                                               uint32_t pieces, uint32_t total,
+                                                               float* __restrict__ out,
+                                                               uint16_t* __restrict__ out_bf16) {
+  constexpr int kBatch = 8;
+  const uint32_t gid = blockIdx.x * blockDim.x + threadIdx.x;
+  if (gid >= total) return;
+  const uint32_t t = gid / pieces;
+  const uint32_t c = gid - t * pieces;
+  float acc[kCols] = {};
+  for (int j0 = 0; j0 < k; j0 += kBatch) {
+    uint32_t v[kBatch][kCols / 2];
+    float w[kBatch];
+    bool ok[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const bool in = j0 + j < k;
+      const int32_t p = in ? pair_index[(int64_t)t * k + j0 + j] : -1;
+      w[j] = in ? weights[(int64_t)t * k + j0 + j] : 0.0f;
+      ok[j] = p >= 0 && p < P;
+#pragma unroll
+      for (int q = 0; q < kCols / 2; ++q) v[j][q] = 0;
+      if (ok[j]) {
+        const uint16_t* src = y + (int64_t)p * H + (int64_t)kCols * c;
+        if constexpr (kCols == 8) {
+          const uint4 r = *reinterpret_cast<const uint4*>(src);
+          v[j][0] = r.x, v[j][1] = r.y, v[j][2] = r.z, v[j][3] = r.w;
+        } else {
+          const uint2 r = *reinterpret_cast<const uint2*>(src);
+          v[j][0] = r.x, v[j][1] = r.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (ok[j])
+#pragma unroll
+        for (int q = 0; q < kCols / 2; ++q) {
+          acc[2 * q] = fmaf(w[j], bf16_lo(v[j][q]), acc[2 * q]);
+          acc[2 * q + 1] = fmaf(w[j], bf16_hi(v[j][q]), acc[2 * q + 1]);
+        }
+  }
+  const int64_t at = (int64_t)t * H + (int64_t)kCols * c;
+#pragma unroll
+  for (int q = 0; q < kCols; q += 4) {
+    if (out) *reinterpret_cast<float4*>(out + at + q) = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
+    if (out_bf16)
+      *reinterpret_cast<uint2*>(out_bf16 + at + q) =
+          make_uint2(bf16x2_rne(acc[q], acc[q + 1]), bf16x2_rne(acc[q + 2], acc[q + 3]));
+  }
+}
+
 }  // namespace
+
+hipError_t launch_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, const int32_t* pair_index,
+                                   const float* weights, int64_t T, int k, float* out, uint16_t* out_bf16,
+                                   hipStream_t stream) {
+  const int cols = H % 8 == 0 ? 8 : 4;
+  const uint32_t pieces = (uint32_t)(H / cols), total = (uint32_t)(T * pieces);
+  const dim3 grid((total + 255) / 256);
+  if (cols == 8)
+    hipLaunchKernelGGL(moe_combine_bf16_kernel<8>, grid, dim3(256), 0, stream, y, P, H, pair_index, weights, k, pieces,
+                       total, out, out_bf16);
+  else
+    hipLaunchKernelGGL(moe_combine_bf16_kernel<4>, grid, dim3(256), 0, stream, y, P, H, pair_index, weights, k, pieces,
+                       total, out, out_bf16);
+  return hipGetLastError();
+}
 
 hipError_t launch_moe_combine(const float* y, int64_t P, int64_t H, const int32_t* pair_index, const float* weights,
                               int64_t T, int k, float* out, uint16_t* out_bf16, hipStream_t stream) {

@@ -1,0 +1,782 @@
+// Plain MXFP4 GEMM on gfx950 scaled MFMA: the dense path next to the two-path
+// GEMM of gemm.hip (one activation operand instead of backbone + residual):
+//   Y[t][o] = sum_k deq(A)[t][k] deq(W)[o][k],
+// dense or per expert segment, stored as fp32 or bf16, or, for a fused gate|up
+// weight, turned into h = bf16(silu(gate) * up) and coded to MXFP4 in the
+// epilogue so that neither Y nor h passes through HBM.
+//
+// V_MFMA_SCALE_F32_32X32X64_F8F6F4 takes the weight rows as its first operand
+// and the activation rows as its second, so a lane's accumulators are 16
+// output columns of ONE token: column 8 (r / 4) + 4 (lane / 32) + r % 4 of the
+// 32-column tile, token lane % 32. Four neighbouring columns then leave in one
+// wide LDS or global store, and the 32 entries of an MXFP4 block of h sit in
+// two lanes (l and l + 32): its amax is one register maximum and one half-wave
+// swap, and its codes need no LDS.
+//
+// Main loop: a ring of LDS stages of 128 K entries, filled by buffer loads
+// that write straight into LDS. The buffer view of an operand is one stage
+// (base moved by the scalar unit, rows past the end read as zero), so offsets
+// stay below 2^31 for any K. The last, partial stage of a K that is no
+// multiple of 128 is whole in memory (zero codes, zero scales).
+
+#include "gemm_common.h"
+#include "sharq_device.h"
+#include "sharq_internal.h"
+#include "silu.h"
+
+namespace sharq {
+namespace {
+
+// Workgroup tile of NWM x NWN waves, each WM x WN MFMA tiles of 32 x 32
+// (WM along the tokens), and the layout of one LDS stage: activation codes,
+// weight codes, weight scales, activation scales (padded to 64 rows, the width
+// of one buffer->LDS load). When the activation's scale runs do not split
+// evenly over the waves the spare instructions read nothing into a trash area
+// at the end, so that every wave issues the same number of loads per stage.
+// WGS workgroups share a CU (bounded by the LDS and by the registers).
+template <int WM_, int WN_, int NWM_, int NWN_, int RING_, int WGS_>
+struct MxTile {
+  static constexpr int WM = WM_, WN = WN_, NWM = NWM_, NWN = NWN_;
+  static constexpr int kWaves = NWM * NWN, kThreads = 64 * kWaves;
+  static constexpr int BM = 32 * WM * NWM, BN = 32 * WN * NWN;
+  static constexpr int kOffA = 0;
+  static constexpr int kOffW = BM * kRowBytes;
+  static constexpr int kOffSW = kOffW + BN * kRowBytes;
+  static constexpr int kOffSA = kOffSW + BN * 4;
+  static constexpr int kAChunks = BM / 16 / kWaves;
+  static constexpr int kWChunks = BN / 16 / kWaves;
+  static constexpr int kARuns = (BM + 63) / 64;
+  static constexpr int kALoads = (kARuns + kWaves - 1) / kWaves;
+  static constexpr int kWLoads = BN / 64 / kWaves;
+  static constexpr int kLoads = kAChunks + kWChunks + kALoads + kWLoads;
+  static constexpr int kStage = kOffSA + 256 * kWaves * kALoads;
+  static_assert(kAChunks * 16 * kWaves == BM && kWChunks * 16 * kWaves == BN, "whole 1 KB chunks per wave");
+  static_assert(kWLoads * 64 * kWaves == BN, "whole scale runs per wave");
+  static constexpr int kRing = RING_;
+  static constexpr int kWavesPerSimd = (WGS_ * kWaves + 3) / 4;
+  static_assert(kRing >= 2 && WGS_ * kRing * kStage <= kLdsBytes, "ring");
+  static_assert(kRing * kStage >= kWaves * 32 * 272, "the epilogue's slabs fit in the ring's LDS");
+  static_assert(WN % 4 == 0 && BN == 256, "a wave holds gate, gate, up, up columns; one tile is 128 h columns");
+};
+using Mx32 = MxTile<1, 4, 1, 2, 3, 2>;
+using Mx64 = MxTile<2, 4, 1, 2, 3, 2>;
+using Mx128 = MxTile<2, 4, 2, 2, 3, 2>;
+using Mx256 = MxTile<4, 4, 2, 2, 4, 1>;
+
+struct MxOperands {
+  const uint8_t* a_codes;   // [G][rows][64]
+  const uint8_t* a_scales;  // [G][rows][4]
+  const uint8_t* w_codes;   // [G][O][64] (grouped: already the expert's)
+  const uint8_t* w_scales;  // [G][O][4]
+  int64_t rows, O;
+  int nsteps;
+};
+
+template <class C>
+struct MxFrags {
+  v8i a[C::WM], w[C::WN];
+};
+template <class C>
+struct MxScales {
+  uint32_t a[C::WM], w[C::WN];
+};
+
+// One LDS read of the schedule: item R < WM + WN is a fragment of sub-step
+// SUB; the next WM + WN items (SUB = 0 only) are the scale dwords. The scale
+// dword of a row holds the bytes of the stage's 4 blocks; shifted right by
+// 8 (lane / 32), byte 0 (sub-step 0) and byte 2 (sub-step 1) are the blocks of
+// the lane's K half.
+template <class C, int SUB, int R>
+__device__ __forceinline__ void mx_read(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
+                                        int lh) {
+  constexpr int kF = C::WM + C::WN;
+  if constexpr (R < C::WM) {
+    f.a[R] = frag(st + C::kOffA + swz(32 * C::WM * wm + 32 * R + lr, 2 * SUB + lh));
+  } else if constexpr (R < kF) {
+    constexpr int j = R - C::WM;
+    f.w[j] = frag(st + C::kOffW + swz(32 * C::WN * wn + 32 * j + lr, 2 * SUB + lh));
+  } else if constexpr (SUB == 0 && R < kF + C::WM) {
+    constexpr int i = R - kF;
+    c.a[i] = *reinterpret_cast<const uint32_t*>(st + C::kOffSA + 4 * (32 * C::WM * wm + 32 * i + lr)) >> (8 * lh);
+  } else if constexpr (SUB == 0 && R < 2 * kF) {
+    constexpr int j = R - kF - C::WM;
+    c.w[j] = *reinterpret_cast<const uint32_t*>(st + C::kOffSW + 4 * (32 * C::WN * wn + 32 * j + lr)) >> (8 * lh);
+  }
+}
+
+template <class C, int R = 0>
+__device__ __forceinline__ void mx_read_first(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
+                                              int lh) {
+  if constexpr (R < 2 * (C::WM + C::WN)) {
+    mx_read<C, 0, R>(st, f, c, wm, wn, lr, lh);
+    mx_read_first<C, R + 1>(st, f, c, wm, wn, lr, lh);
+  }
+}
+
+// MFMA number M of a sub-step. kSkip: row blocks from `active` on hold no
+// valid row (a partial last tile of an expert segment) and are skipped.
+template <class C, int SUB, int M, bool kSkip>
+__device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
+                                        int active) {
+  constexpr int i = M / C::WN, j = M % C::WN;
+  if (!kSkip || i < active)
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[j], f.a[i], acc[i][j], 4, 4, 2 * SUB,
+                                                                (int)c.w[j], 2 * SUB, (int)c.a[i]);
+}
+
+template <class C>
+struct MxLoader {
+  const uint8_t *a_codes, *w_codes, *a_scales, *w_scales;  // base of the next stage to load
+  uint32_t a_off[C::kAChunks];  // byte offset of this lane's A code chunk inside a stage, kOOB if absent
+  uint32_t w_off[C::kWChunks];
+  uint32_t sw_off[C::kWLoads];  // this lane's scale dword
+  uint32_t sa_off[C::kALoads];
+  int wave;
+  int left;  // stages not yet issued; batches past the last one read nothing
+  uint32_t a_rows, w_rows;
+
+  struct Dest {
+    uint32_t base;
+    i32x4 a, w, sa, sw;
+  };
+  // Buffer views of the next stage and its LDS slot; moves on to the stage after.
+  __device__ __forceinline__ Dest next(uint8_t* st) {
+    const uint32_t na = left > 0 ? a_rows : 0, nw = left > 0 ? w_rows : 0;
+    Dest d;
+    d.base = lds_offset(st);
+    d.a = make_rsrc(a_codes, (int64_t)na * kRowBytes);
+    d.w = make_rsrc(w_codes, (int64_t)nw * kRowBytes);
+    d.sa = make_rsrc(a_scales, (int64_t)na * 4);
+    d.sw = make_rsrc(w_scales, (int64_t)nw * 4);
+    --left;
+    a_codes += (int64_t)a_rows * kRowBytes;
+    w_codes += (int64_t)w_rows * kRowBytes;
+    a_scales += (int64_t)a_rows * 4;
+    w_scales += (int64_t)w_rows * 4;
+    return d;
+  }
+
+  template <int J>
+  __device__ __forceinline__ void issue(const Dest& d) const {
+    if constexpr (J < C::kAChunks) {
+      buffer_to_lds16(d.a, a_off[J], d.base + C::kOffA + 1024 * (wave + C::kWaves * J));
+    } else if constexpr (J < C::kAChunks + C::kWChunks) {
+      constexpr int j = J - C::kAChunks;
+      buffer_to_lds16(d.w, w_off[j], d.base + C::kOffW + 1024 * (wave + C::kWaves * j));
+    } else if constexpr (J < C::kAChunks + C::kWChunks + C::kWLoads) {
+      constexpr int i = J - C::kAChunks - C::kWChunks;
+      buffer_to_lds4(d.sw, sw_off[i], d.base + C::kOffSW + 256 * (wave + C::kWaves * i));
+    } else if constexpr (J < C::kLoads) {
+      constexpr int i = J - C::kAChunks - C::kWChunks - C::kWLoads;
+      buffer_to_lds4(d.sa, sa_off[i], d.base + C::kOffSA + 256 * (wave + C::kWaves * i));
+    }
+  }
+  template <int J = 0>
+  __device__ __forceinline__ void issue_all(const Dest& d) const {
+    if constexpr (J < C::kLoads) {
+      issue<J>(d);
+      issue_all<J + 1>(d);
+    }
+  }
+};
+
+// First half of an iteration: the sub-step 0 MFMAs of the stage, each followed
+// by one fragment read of its sub-step 1.
+template <class C, int M, bool kSkip>
+__device__ __forceinline__ void mx_first_half(const MxFrags<C>& f0, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
+                                              const uint8_t* cur, MxFrags<C>& f1, MxScales<C>& unused, int wm, int wn,
+                                              int lr, int lh, int active) {
+  constexpr int kF = C::WM + C::WN, kM = C::WM * C::WN;
+  if constexpr (M < kM || M < kF) {
+    if constexpr (M < kM) mx_mfma<C, 0, M, kSkip>(f0, c, acc, active);
+    mx_read<C, 1, M>(cur, f1, unused, wm, wn, lr, lh);
+    __builtin_amdgcn_sched_barrier(0);
+    mx_first_half<C, M + 1, kSkip>(f0, c, acc, cur, f1, unused, wm, wn, lr, lh, active);
+  }
+}
+
+// Second half, after the wait for the next stage and the barrier that frees
+// this stage's slot: the sub-step 1 MFMAs, each followed by one load of the
+// stage that goes into the freed slot and one LDS read of the next stage.
+template <class C, int M, bool kSkip>
+__device__ __forceinline__ void mx_second_half(const MxFrags<C>& f1, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
+                                               const MxLoader<C>& ld, const typename MxLoader<C>::Dest& d,
+                                               const uint8_t* next, MxFrags<C>& f0, MxScales<C>& cn, int wm, int wn,
+                                               int lr, int lh, int active) {
+  constexpr int kM = C::WM * C::WN, kItems = 2 * (C::WM + C::WN);
+  if constexpr (M < kM || M < C::kLoads || M < kItems) {
+    if constexpr (M < kM) mx_mfma<C, 1, M, kSkip>(f1, c, acc, active);
+    ld.template issue<M>(d);
+    mx_read<C, 0, M>(next, f0, cn, wm, wn, lr, lh);
+    __builtin_amdgcn_sched_barrier(0);
+    mx_second_half<C, M + 1, kSkip>(f1, c, acc, ld, d, next, f0, cn, wm, wn, lr, lh, active);
+  }
+}
+
+// acc += the product over stages [s_begin, s_end) (s_begin < s_end).
+template <class C, bool kSkip>
+__device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows& tr, const TileCols& tc,
+                                            uint8_t* ring, v16f (&acc)[C::WM][C::WN], int s_begin, int s_end) {
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::NWM, wn = wave / C::NWM;
+  const int lr = lane & 31, lh = lane >> 5;
+  const int64_t first_row = 32 * C::WM * wm;
+  const int active = __builtin_amdgcn_readfirstlane(
+      !kSkip ? C::WM
+      : tr.rows_valid <= first_row ? 0
+      : (int)min<int64_t>((tr.rows_valid - first_row + 31) / 32, C::WM));
+
+  MxLoader<C> ld;
+  ld.wave = wave;
+  ld.left = s_end - s_begin;
+  ld.a_rows = (uint32_t)op.rows;
+  ld.w_rows = (uint32_t)op.O;
+  ld.a_codes = op.a_codes + (int64_t)s_begin * op.rows * kRowBytes;
+  ld.w_codes = op.w_codes + (int64_t)s_begin * op.O * kRowBytes;
+  ld.a_scales = op.a_scales + (int64_t)s_begin * op.rows * 4;
+  ld.w_scales = op.w_scales + (int64_t)s_begin * op.O * 4;
+  // A lane fills a fixed LDS chunk; it reads the global chunk that belongs there after the swizzle.
+#pragma unroll
+  for (int j = 0; j < C::kAChunks; ++j) {
+    const int row = 16 * (wave + C::kWaves * j) + (lane >> 2);
+    const int64_t src = tr.src(row);
+    ld.a_off[j] = src >= 0 ? (uint32_t)(src * kRowBytes + ((lane & 3) ^ swz_part(row)) * 16) : kOOB;
+  }
+#pragma unroll
+  for (int j = 0; j < C::kWChunks; ++j) {
+    const int row = 16 * (wave + C::kWaves * j) + (lane >> 2);
+    const int64_t o = tc.w_row(row);
+    ld.w_off[j] = o < op.O ? (uint32_t)(o * kRowBytes + ((lane & 3) ^ swz_part(row)) * 16) : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < C::kWLoads; ++i) {
+    const int64_t o = tc.w_row(64 * (wave + C::kWaves * i) + lane);
+    ld.sw_off[i] = o < op.O ? (uint32_t)(o * 4) : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < C::kALoads; ++i) {
+    const int q = wave + C::kWaves * i;  // a spare instruction (q >= kARuns) reads nothing
+    const int64_t src = q < C::kARuns ? tr.src(64 * q + lane) : -1;
+    ld.sa_off[i] = src >= 0 ? (uint32_t)(src * 4) : kOOB;
+  }
+
+#pragma unroll
+  for (int b = 0; b < C::kRing; ++b) ld.issue_all(ld.next(ring + b * C::kStage));
+  wait_vmcnt<(C::kRing - 1) * C::kLoads>();  // the first batch landed
+  ring_barrier();
+  MxFrags<C> f0, f1;
+  MxScales<C> c, cn;
+  mx_read_first<C>(ring, f0, c, wm, wn, lr, lh);
+  int slot = 0;
+#pragma unroll 1
+  for (int s = s_begin; s < s_end; ++s) {
+    uint8_t* cur = ring + slot * C::kStage;
+    slot = slot + 1 == C::kRing ? 0 : slot + 1;
+    const uint8_t* next = ring + slot * C::kStage;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    mx_first_half<C, 0, kSkip>(f0, c, acc, cur, f1, cn, wm, wn, lr, lh, active);
+    __builtin_amdgcn_s_setprio(0);
+    wait_vmcnt<(C::kRing - 2) * C::kLoads>();  // the next stage landed; later batches may be in flight
+    ring_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const typename MxLoader<C>::Dest d = ld.next(cur);
+    __builtin_amdgcn_s_setprio(1);
+    mx_second_half<C, 0, kSkip>(f1, c, acc, ld, d, next, f0, cn, wm, wn, lr, lh, active);
+    __builtin_amdgcn_s_setprio(0);
+    c = cn;
+  }
+  wait_vmcnt<0>();  // the trailing batches, before the LDS is used again
+}
+
+template <class C>
+__device__ __forceinline__ void mx_zero(v16f (&acc)[C::WM][C::WN]) {
+#pragma unroll
+  for (int i = 0; i < C::WM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::WN; ++j) acc[i][j] = v16f{};
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues
+// ---------------------------------------------------------------------------
+
+constexpr int kSlabStride = 272;  // 256 bytes of a row + 16, so that rows start on distinct banks
+
+// Store the tile to y (fp32, or bf16 rounded to nearest even). A wave turns
+// slabs of 32 tokens x 256 bytes (64 fp32 or 128 bf16 columns) through LDS of
+// its own, so that every global store is 16 bytes a lane in 256-byte row runs.
+// wide: y rows are 16-byte aligned (leading dimension included).
+template <class C, class Out>
+__device__ __forceinline__ void mx_store(const v16f (&acc)[C::WM][C::WN], uint8_t* lds, Out* __restrict__ y,
+                                         int64_t ldy, const TileRows& tr, int64_t n0, int64_t O, bool wide) {
+  constexpr bool kBf16 = sizeof(Out) == 2;
+  constexpr int kJ = kBf16 ? 4 : 2;         // MFMA column tiles of a slab
+  constexpr int kPer = 16 / sizeof(Out);    // columns of a 16-byte piece
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave % C::NWM, wn = wave / C::NWM;
+  const int lr = lane & 31, lh = lane >> 5;
+  ring_barrier();  // every wave is done with the ring
+  uint8_t* slab = lds + wave * 32 * kSlabStride;
+#pragma unroll
+  for (int i = 0; i < C::WM; ++i) {
+    const int row0 = 32 * C::WM * wm + 32 * i;
+    if (row0 >= tr.rows_valid) break;  // wave-uniform
+#pragma unroll
+    for (int j0 = 0; j0 < C::WN; j0 += kJ) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const v16f& a = acc[i][j0 + j];
+          const int col = 32 * j + 8 * g + 4 * lh;
+          if constexpr (kBf16) {
+            *reinterpret_cast<uint2*>(slab + lr * kSlabStride + 2 * col) =
+                make_uint2(bf16x2_rne(a[4 * g], a[4 * g + 1]), bf16x2_rne(a[4 * g + 2], a[4 * g + 3]));
+          } else {
+            *reinterpret_cast<float4*>(slab + lr * kSlabStride + 4 * col) =
+                make_float4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]);
+          }
+        }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int r = 4 * q + (lane >> 4), piece = lane & 15;
+        const uint4 v = *reinterpret_cast<const uint4*>(slab + r * kSlabStride + 16 * piece);
+        const int64_t o = n0 + 32 * (C::WN * wn + j0) + kPer * piece;
+        if (row0 + r < tr.rows_valid) {
+          Out* dst = y + (tr.m0 + row0 + r) * ldy + o;
+          if (wide && o + kPer <= O) {
+            *reinterpret_cast<uint4*>(dst) = v;
+          } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (o + e < O) {
+                if constexpr (kBf16)
+                  dst[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+                else
+                  dst[e] = __uint_as_float(w[e]);
+              }
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+struct MxH {
+  uint8_t* codes;   // [ceil(I / 128)][T][64]
+  uint8_t* scales;  // [ceil(I / 128)][T][4]
+  int64_t T, I;
+};
+
+// 16 values of a block in the accumulator order of one lane (four runs of four
+// neighbouring columns) -> 8 bytes of E2M1 codes, a run of four per 16 bits.
+__device__ __forceinline__ void quantize16(const float (&v)[16], float scale, uint32_t (&w)[2]) {
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * d + 0], v[8 * d + 1], scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * d + 2], v[8 * d + 3], scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * d + 4], v[8 * d + 5], scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * d + 6], v[8 * d + 7], scale, 3);
+    w[d] = r;
+  }
+}
+
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+
+// The pair (x of lane l % 32, y of lane l % 32 + 32) of two registers: lanes
+// below 32 get x's two halves, lanes from 32 on y's.
+__device__ __forceinline__ v2u half_swap(uint32_t x, uint32_t y) {
+  return __builtin_amdgcn_permlane32_swap(x, y, false, false);
+}
+
+// h = bf16(silu(gate) * up) of the tile, coded to MXFP4: a wave's four MFMA
+// column tiles are gate, gate, up, up of 64 h columns, i.e. two blocks of each
+// of its tokens. Lane l holds half of both blocks of token l % 32; after the
+// half-wave swap it holds all of block l / 32 and writes its 16 bytes.
+template <class C>
+__device__ __forceinline__ void mx_silu_store(const v16f (&acc)[C::WM][C::WN], const TileRows& tr, int64_t h0,
+                                              const MxH& out) {
+  static_assert(C::WN == 4, "gate, gate, up, up");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave % C::NWM, wn = wave / C::NWM;
+  const int lr = lane & 31, lh = lane >> 5;
+  const int64_t block = (h0 >> 5) + 2 * wn + lh;  // the block this lane writes
+  const int64_t blocks = out.I >> 5, padded = (blocks + 3) & ~(int64_t)3;
+#pragma unroll
+  for (int i = 0; i < C::WM; ++i) {
+    const int row = 32 * C::WM * wm + 32 * i + lr;
+    uint32_t code[2][2], amax[2], byte[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float h[16], m = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const uint32_t b = bf16x2_rne(silu_times(acc[i][j][r], acc[i][j + 2][r]),
+                                      silu_times(acc[i][j][r + 1], acc[i][j + 2][r + 1]));
+        h[r] = bf16_lo(b);
+        h[r + 1] = bf16_hi(b);
+        m = fmaxf(m, fmaxf(fabsf(h[r]), fabsf(h[r + 1])));
+      }
+      const v2u both = half_swap(__float_as_uint(m), __float_as_uint(m));
+      amax[j] = max(both[0], both[1]);  // non-negative floats order as their bits
+      byte[j] = e8m0_from_amax_bits(amax[j]);
+      quantize16(h, scale_from_e8m0(byte[j]), code[j]);
+    }
+    const v2u lo = half_swap(code[0][0], code[1][0]);  // [0]: columns 0-3, 8-11; [1]: columns 4-7, 12-15
+    const v2u hi = half_swap(code[0][1], code[1][1]);  // the same from column 16 on
+    if (row < tr.rows_valid && block < padded) {
+      const int64_t t = tr.m0 + row;
+      const bool real = block < blocks;
+      const uint4 c = make_uint4((lo[0] & 0xFFFFu) | (lo[1] << 16), (lo[0] >> 16) | (lo[1] & 0xFFFF0000u),
+                                 (hi[0] & 0xFFFFu) | (hi[1] << 16), (hi[0] >> 16) | (hi[1] & 0xFFFF0000u));
+      *reinterpret_cast<uint4*>(out.codes + code_offset(t, (uint32_t)block, out.T)) =
+          real ? c : make_uint4(0, 0, 0, 0);
+      out.scales[scale_index(t, (uint32_t)block, out.T)] = (uint8_t)(real ? (lh ? byte[1] : byte[0]) : 0u);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Kernels
+// ---------------------------------------------------------------------------
+
+#define SHARQ_MX_LDS(C) __shared__ __attribute__((aligned(16))) uint8_t lds[C::kRing * C::kStage];
+
+__device__ __forceinline__ TileRows dense_rows(int64_t m0, int64_t T, int bm) {
+  TileRows tr;
+  tr.m0 = m0;
+  tr.rows_valid = T - m0 < bm ? T - m0 : bm;
+  tr.gather = nullptr;
+  tr.src_rows = T;
+  return tr;
+}
+
+template <class C, class Out>
+__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_linear_kernel(MxOperands op, Out* __restrict__ y,
+                                                                               int64_t ldy, bool wide, int tiles_m,
+                                                                               int tiles_total) {
+  SHARQ_MX_LDS(C)
+  const TileIndex ti = tile_index(blockIdx.x, tiles_m, tiles_total);
+  const TileRows tr = dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM);
+  const int64_t n0 = (int64_t)ti.tn * C::BN;
+  v16f acc[C::WM][C::WN];
+  mx_zero<C>(acc);
+  mx_mainloop<C, false>(op, tr, TileCols{n0, 0}, lds, acc, 0, op.nsteps);
+  mx_store<C, Out>(acc, lds, y, ldy, tr, n0, op.O, wide);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_linear_silu_kernel(MxOperands op, MxH out,
+                                                                                    int tiles_m, int tiles_total) {
+  SHARQ_MX_LDS(C)
+  const TileIndex ti = tile_index(blockIdx.x, tiles_m, tiles_total);
+  const TileRows tr = dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM);
+  const int64_t h0 = (int64_t)ti.tn * 128;
+  v16f acc[C::WM][C::WN];
+  mx_zero<C>(acc);
+  mx_mainloop<C, false>(op, tr, TileCols{h0, out.I}, lds, acc, 0, op.nsteps);
+  mx_silu_store<C>(acc, tr, h0, out);
+}
+
+// Split-K: item q of the S * tiles work items computes split q / tiles (stages
+// [split * nsteps / S, (split + 1) * nsteps / S)) of tile q % tiles and stores
+// its fp32 partial in partials[split] ([S][T][O]). The reduce kernels add the
+// partials in split order, so results do not depend on timing; the kernel
+// boundary makes them visible to every XCD.
+template <class C>
+__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_split_kernel(MxOperands op, int tiles_m,
+                                                                              int tiles_total, int S, bool wide,
+                                                                              float* __restrict__ partials) {
+  SHARQ_MX_LDS(C)
+  const int item = xcd_item(blockIdx.x, tiles_total * S);
+  const int split = item / tiles_total;
+  const TileIndex ti = tile_order(item - split * tiles_total, tiles_m, tiles_total);
+  const TileRows tr = dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM);
+  const int64_t n0 = (int64_t)ti.tn * C::BN;
+  v16f acc[C::WM][C::WN];
+  mx_zero<C>(acc);
+  const int s0 = (int)((int64_t)split * op.nsteps / S), s1 = (int)((int64_t)(split + 1) * op.nsteps / S);
+  mx_mainloop<C, false>(op, tr, TileCols{n0, 0}, lds, acc, s0, s1);
+  mx_store<C, float>(acc, lds, partials + (int64_t)split * op.rows * op.O, op.O, tr, n0, op.O, wide);
+}
+
+constexpr int kMxMaxSplits = 16;
+
+__device__ __forceinline__ void store_out(float* y, float v) { *y = v; }
+__device__ __forceinline__ void store_out(uint16_t* y, float v) { *y = (uint16_t)bf16_rne_bits(v); }
+
+template <class Out>
+__global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict__ partials, int S, int64_t T,
+                                                        int64_t O, Out* __restrict__ y, int64_t ldy) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= T * O) return;
+  const int64_t t = e / O, o = e - t * O;
+  float part[kMxMaxSplits];
+#pragma unroll
+  for (int q = 0; q < kMxMaxSplits; ++q) part[q] = q < S ? partials[(int64_t)q * T * O + e] : 0.0f;
+  float v = part[0];
+#pragma unroll
+  for (int q = 1; q < kMxMaxSplits; ++q)
+    if (q < S) v += part[q];
+  store_out(y + t * ldy + o, v);
+}
+
+// The reduce of a split gate|up product with the SiLU and the coding of h:
+// half-wave lane l of a row's block owns column l, so a block's gate and up
+// runs are 128 contiguous bytes a partial. Blocks of a partial last stage are
+// written as zeros.
+__global__ __launch_bounds__(256) void mx_reduce_silu_kernel(const float* __restrict__ partials, int S, MxH out) {
+  const int64_t blocks = out.I >> 5, padded = (blocks + 3) & ~(int64_t)3;
+  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int col = threadIdx.x & 31;
+  const int64_t t = unit / padded, b = unit - t * padded;
+  if (t >= out.T) return;  // whole half-waves
+  float h = 0.0f;
+  if (b < blocks) {
+    const int64_t plane = out.T * 2 * out.I;
+    const float* src = partials + t * 2 * out.I + 32 * b + col;
+    float g[kMxMaxSplits], u[kMxMaxSplits];
+#pragma unroll
+    for (int q = 0; q < kMxMaxSplits; ++q) {
+      g[q] = q < S ? src[q * plane] : 0.0f;
+      u[q] = q < S ? src[q * plane + out.I] : 0.0f;
+    }
+    float gs = g[0], us = u[0];
+#pragma unroll
+    for (int q = 1; q < kMxMaxSplits; ++q)
+      if (q < S) gs += g[q], us += u[q];
+    h = __uint_as_float(bf16_rne_bits(silu_times(gs, us)) << 16);
+  }
+  float m = fabsf(h);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 32));
+  const uint32_t byte = b < blocks ? e8m0_from_amax_bits(__float_as_uint(m)) : 0u;
+  const float other = __shfl_xor(h, 1, 32);
+  uint32_t code = 0;
+  code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, h, other, scale_from_e8m0(byte), 0);  // even columns
+  if ((col & 1) == 0) out.codes[code_offset(t, (uint32_t)b, out.T) + (col >> 1)] = (uint8_t)code;
+  if (col == 0) out.scales[scale_index(t, (uint32_t)b, out.T)] = (uint8_t)byte;
+}
+
+__device__ __forceinline__ void mx_select_expert(MxOperands& op, int e) {
+  op.w_codes += (int64_t)e * op.O * kRowBytes * op.nsteps;
+  op.w_scales += (int64_t)e * op.O * 4 * op.nsteps;
+}
+
+template <class C, class Out>
+__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_grouped_kernel(
+    MxOperands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, Out* __restrict__ y,
+    int64_t P, bool wide, int tiles_n) {
+  SHARQ_MX_LDS(C)
+  const GroupedTile g = grouped_tile<C, false>(seg, E, P, a_rows, op.rows, tiles_n);
+  if (g.e < 0) return;  // uniform across the workgroup
+  mx_select_expert(op, g.e);
+  const int64_t n0 = (int64_t)g.col * C::BN;
+  v16f acc[C::WM][C::WN];
+  mx_zero<C>(acc);
+  mx_mainloop<C, true>(op, g.tr, TileCols{n0, 0}, lds, acc, 0, op.nsteps);
+  mx_store<C, Out>(acc, lds, y, op.O, g.tr, n0, op.O, wide);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_grouped_silu_kernel(
+    MxOperands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, MxH out, int tiles_n) {
+  SHARQ_MX_LDS(C)
+  const GroupedTile g = grouped_tile<C, true>(seg, E, out.T, a_rows, op.rows, tiles_n);
+  if (g.e < 0) return;
+  mx_select_expert(op, g.e);
+  const int64_t h0 = (int64_t)g.col * 128;
+  v16f acc[C::WM][C::WN];
+  mx_zero<C>(acc);
+  mx_mainloop<C, true>(op, g.tr, TileCols{h0, out.I}, lds, acc, 0, op.nsteps);
+  mx_silu_store<C>(acc, g.tr, h0, out);
+}
+
+// ---------------------------------------------------------------------------
+// Launch
+// ---------------------------------------------------------------------------
+
+MxOperands mx_operands(const MxProduct& p) {
+  return MxOperands{p.a_codes, p.a_scales, p.w_codes, p.w_scales, p.rows, p.O, (int)((p.K + 127) / 128)};
+}
+
+// Row tile of a dense product: 0 Mx32, 1 Mx64, 2 Mx128, 3 Mx256.
+int mx_row_tile(int64_t T, int64_t O) {
+  if (T <= 32) return 0;
+  if (T <= 64) return 1;
+  return (T + 255) / 256 * ((O + 255) / 256) >= 256 ? 3 : 2;
+}
+int64_t mx_tile_rows(int tile) { return tile == 0 ? 32 : tile == 1 ? 64 : tile == 2 ? 128 : 256; }
+
+struct MxPlan {
+  int tile, S;
+  int tiles_m, tiles_total;
+};
+
+MxPlan mx_plan(int64_t T, int64_t O, int64_t K, bool may_split) {
+  MxPlan p{mx_row_tile(T, O), 1, 0, 0};
+  const int64_t bm = mx_tile_rows(p.tile);
+  p.tiles_m = (int)((T + bm - 1) / bm);
+  p.tiles_total = p.tiles_m * (int)((O + 255) / 256);
+  if (!may_split || p.tile == 3) return p;
+  const int64_t nsteps = (K + 127) / 128;
+  const int64_t s_max = nsteps / 4 < kMxMaxSplits ? nsteps / 4 : kMxMaxSplits;
+  double best = 0;
+  for (int64_t s = 1; s <= s_max && (s == 1 || s * T * O * 4 <= ((int64_t)256 << 20)); ++s) {
+    const double c = p.tile == 0 ? 0.40 : p.tile == 1 ? 0.45 : 0.55;
+    const int64_t per_cu = (s * p.tiles_total + 255) / 256;
+    const double crowd = per_cu <= 1 ? 1.0 : 1.7 * (double)per_cu / 2.0;
+    const double loop = (double)nsteps / (double)s * c * crowd;
+    const double stream = ((double)O * (double)K + (double)T * (double)K) * 17.0 / 32.0 / 6.5e6;
+    double t = loop > stream ? loop : stream;
+    if (s > 1) t += 2.0 + (double)(2 * s + 1) * (double)T * (double)O * 4.0 / 4.0e6;
+    if (s == 1 || t < best) best = t, p.S = (int)s;
+  }
+  return p;
+}
+
+bool mx_wide(const void* y, int64_t ldy, int64_t bytes) {
+  return (reinterpret_cast<uintptr_t>(y) & 15) == 0 && ldy * bytes % 16 == 0;
+}
+
+template <class Out>
+void launch_mx_store(const MxPlan& p, const MxOperands& op, Out* y, int64_t ldy, hipStream_t stream) {
+  const bool wide = mx_wide(y, ldy, sizeof(Out));
+#define SHARQ_MX(C)                                                                                               \
+  hipLaunchKernelGGL((mx_linear_kernel<C, Out>), dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, y, ldy,  \
+                     wide, p.tiles_m, p.tiles_total)
+  if (p.tile == 0) SHARQ_MX(Mx32);
+  else if (p.tile == 1) SHARQ_MX(Mx64);
+  else if (p.tile == 2) SHARQ_MX(Mx128);
+  else SHARQ_MX(Mx256);
+#undef SHARQ_MX
+}
+
+void launch_mx_split(const MxPlan& p, const MxOperands& op, float* partials, hipStream_t stream) {
+  const bool wide = op.O % 4 == 0;
+#define SHARQ_MX(C)                                                                                              \
+  hipLaunchKernelGGL(mx_split_kernel<C>, dim3(p.tiles_total* p.S), dim3(C::kThreads), 0, stream, op, p.tiles_m, \
+                     p.tiles_total, p.S, wide, partials)
+  if (p.tile == 0) SHARQ_MX(Mx32);
+  else if (p.tile == 1) SHARQ_MX(Mx64);
+  else SHARQ_MX(Mx128);
+#undef SHARQ_MX
+}
+
+// Row tile of a grouped product, from the mean rows of an expert.
+int mx_grouped_tile(int64_t P, int32_t E) { return P <= 16 * (int64_t)E ? 0 : P <= 64 * (int64_t)E ? 1 : 2; }
+
+}  // namespace
+
+int64_t mx_linear_workspace_bytes(int64_t T, int64_t O, int64_t K) {
+  if (T <= 0 || O <= 0) return 0;
+  const MxPlan p = mx_plan(T, O, K, true);
+  return p.S > 1 ? (int64_t)p.S * T * O * 4 : 0;
+}
+
+hipError_t launch_mx_linear(const MxProduct& m, void* y, int64_t ldy, bool bf16, void* workspace,
+                            int64_t workspace_bytes, hipStream_t stream) {
+  const MxOperands op = mx_operands(m);
+  const int64_t need = mx_linear_workspace_bytes(m.rows, m.O, m.K);
+  const bool split = need > 0 && workspace && workspace_bytes >= need;
+  const MxPlan p = mx_plan(m.rows, m.O, m.K, split);
+  if (!split) {
+    if (bf16) launch_mx_store(p, op, static_cast<uint16_t*>(y), ldy, stream);
+    else launch_mx_store(p, op, static_cast<float*>(y), ldy, stream);
+    return hipGetLastError();
+  }
+  float* partials = static_cast<float*>(workspace);
+  launch_mx_split(p, op, partials, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((m.rows * m.O + 255) / 256));
+  if (bf16)
+    hipLaunchKernelGGL(mx_reduce_kernel<uint16_t>, grid, dim3(256), 0, stream, partials, p.S, m.rows, m.O,
+                       static_cast<uint16_t*>(y), ldy);
+  else
+    hipLaunchKernelGGL(mx_reduce_kernel<float>, grid, dim3(256), 0, stream, partials, p.S, m.rows, m.O,
+                       static_cast<float*>(y), ldy);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_linear_silu(const MxProduct& m, uint8_t* h_codes, uint8_t* h_scales, void* workspace,
+                                 int64_t workspace_bytes, hipStream_t stream) {
+  const MxOperands op = mx_operands(m);
+  const MxH out{h_codes, h_scales, m.rows, m.O / 2};
+  const int64_t need = mx_linear_workspace_bytes(m.rows, m.O, m.K);
+  const bool split = need > 0 && workspace && workspace_bytes >= need;
+  MxPlan p = mx_plan(m.rows, m.O, m.K, split);
+  if (split) {
+    float* partials = static_cast<float*>(workspace);
+    launch_mx_split(p, op, partials, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t units = m.rows * ((out.I / 32 + 3) & ~(int64_t)3);
+    hipLaunchKernelGGL(mx_reduce_silu_kernel, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, stream, partials, p.S,
+                       out);
+    return hipGetLastError();
+  }
+  const int tiles_n = (int)((out.I + 127) / 128);
+  p.tiles_total = p.tiles_m * tiles_n;
+#define SHARQ_MX(C)                                                                                                 \
+  hipLaunchKernelGGL(mx_linear_silu_kernel<C>, dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, out, p.tiles_m, \
+                     p.tiles_total)
+  if (p.tile == 0) SHARQ_MX(Mx32);
+  else if (p.tile == 1) SHARQ_MX(Mx64);
+  else if (p.tile == 2) SHARQ_MX(Mx128);
+  else SHARQ_MX(Mx256);
+#undef SHARQ_MX
+  return hipGetLastError();
+}
+
+int64_t mx_grouped_workgroups(int64_t P, int32_t E, int64_t tiles_n) {
+  const int64_t bm = mx_tile_rows(mx_grouped_tile(P, E));
+  return ((P + bm - 1) / bm + E) * tiles_n;
+}
+
+hipError_t launch_mx_grouped(const MxProduct& m, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
+                             void* y, bool bf16, hipStream_t stream) {
+  const MxOperands op = mx_operands(m);
+  const int tiles_n = (int)((m.O + 255) / 256), tile = mx_grouped_tile(P, E);
+  const dim3 grid((unsigned)mx_grouped_workgroups(P, E, tiles_n));
+  const bool wide = mx_wide(y, m.O, bf16 ? 2 : 4);
+#define SHARQ_MX(C)                                                                                                  \
+  do {                                                                                                               \
+    if (bf16)                                                                                                        \
+      hipLaunchKernelGGL((mx_grouped_kernel<C, uint16_t>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, \
+                         static_cast<uint16_t*>(y), P, wide, tiles_n);                                               \
+    else                                                                                                             \
+      hipLaunchKernelGGL((mx_grouped_kernel<C, float>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E,    \
+                         static_cast<float*>(y), P, wide, tiles_n);                                                  \
+  } while (0)
+  if (tile == 0) SHARQ_MX(Mx32);
+  else if (tile == 1) SHARQ_MX(Mx64);
+  else SHARQ_MX(Mx128);
+#undef SHARQ_MX
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_grouped_silu(const MxProduct& m, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
+                                  uint8_t* h_codes, uint8_t* h_scales, hipStream_t stream) {
+  const MxOperands op = mx_operands(m);
+  const MxH out{h_codes, h_scales, P, m.O / 2};
+  const int tiles_n = (int)((out.I + 127) / 128), tile = mx_grouped_tile(P, E);
+  const dim3 grid((unsigned)mx_grouped_workgroups(P, E, tiles_n));
+#define SHARQ_MX(C)                                                                                            \
+  hipLaunchKernelGGL(mx_grouped_silu_kernel<C>, grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, out, \
+                     tiles_n)
+  if (tile == 0) SHARQ_MX(Mx32);
+  else if (tile == 1) SHARQ_MX(Mx64);
+  else SHARQ_MX(Mx128);
+#undef SHARQ_MX
+  return hipGetLastError();
+}
+
+}  // namespace sharq

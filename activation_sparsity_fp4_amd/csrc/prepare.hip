@@ -28,28 +28,38 @@
 namespace sharq {
 
 // Selection, quantisation and the stores of one block of x'. kLowBits: x'
-// may carry more than bf16's 8 significant bits (a product with gamma).
+// may carry more than bf16's 8 significant bits (a product with gamma). N = 0
+// is the plain coding of the block: no mask, no residual.
 template <int N, int M, bool kLowBits>
 __device__ __forceinline__ void prepare_store(const float (&xv)[32], uint32_t t, uint32_t b,
                                               uint32_t blocks_per_row, uint32_t rows,
                                               uint8_t* __restrict__ bb_codes, uint8_t* __restrict__ bb_scales,
                                               uint8_t* __restrict__ res_codes, uint8_t* __restrict__ res_scales,
                                               uint8_t* __restrict__ mask_out) {
-  const PreparedBlock pb = prepare_block<N, M, kLowBits>(xv);
-  *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = pb.c_bb;
-  *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = pb.c_rs;
-  bb_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_bb;
-  res_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_rs;
-  if (mask_out) reinterpret_cast<uint32_t*>(mask_out)[(int64_t)t * blocks_per_row + b] = pb.keep;
+  if constexpr (N == 0) {
+    const uint32_t e = e8m0_from_amax_bits(amax_bits32(xv));
+    *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = quantize32(xv, scale_from_e8m0(e));
+    bb_scales[scale_index(t, b, rows)] = (uint8_t)e;
+  } else {
+    const PreparedBlock pb = prepare_block<N, M, kLowBits>(xv);
+    *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = pb.c_bb;
+    *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = pb.c_rs;
+    bb_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_bb;
+    res_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_rs;
+    if (mask_out) reinterpret_cast<uint32_t*>(mask_out)[(int64_t)t * blocks_per_row + b] = pb.keep;
+  }
 }
 
+template <int N>
 __device__ __forceinline__ void zero_block(uint32_t t, uint32_t b, uint32_t rows, uint8_t* __restrict__ bb_codes,
                                            uint8_t* __restrict__ bb_scales, uint8_t* __restrict__ res_codes,
                                            uint8_t* __restrict__ res_scales) {
   *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
-  *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
   bb_scales[scale_index(t, b, rows)] = 0;
-  res_scales[scale_index(t, b, rows)] = 0;
+  if constexpr (N != 0) {
+    *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
+    res_scales[scale_index(t, b, rows)] = 0;
+  }
 }
 
 // The whole operator without the norm: x' = x (times gamma when given).
@@ -96,7 +106,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(
       prepare_store<N, M, kGamma>(xv, lb.t, lb.b, blocks_per_row, rows, bb_codes, bb_scales, res_codes,
                                   res_scales, mask_out);
     } else if (lb.row_ok) {
-      zero_block(lb.t, lb.b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+      zero_block<N>(lb.t, lb.b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
     }
     item = next;
     lb = nb;
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(256) void prepare_rms_rows_kernel(
       root = q == 0 ? chunk : root + chunk;
     }
     const float r = (float)(1.0 / sqrt(root / (double)K + (double)eps));
-    if (lane == 0) r_out[t] = r;
+    if (lane == 0 && (N != 0 || r_out)) r_out[t] = r;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const uint32_t b = lane + 64 * q;
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(256) void prepare_rms_rows_kernel(
         }
         prepare_store<N, M, kGamma>(xv, t, b, nb, rows, bb_codes, bb_scales, res_codes, res_scales, mask_out);
       } else if (b < nblk_padded) {
-        zero_block(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+        zero_block<N>(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
       }
     }
     t = next;
@@ -324,7 +334,7 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
       const float r = (float)(1.0 / sqrt(root / (double)K + (double)eps));
       r_row[wave] = r;
       const uint32_t tw = blockIdx.x * kRmsRows + wave;
-      if (tw < rows) r_out[tw] = r;
+      if (tw < rows && (N != 0 || r_out)) r_out[tw] = r;
     }
   }
   __syncthreads();
@@ -335,7 +345,7 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
     const uint32_t b = chunk_block(c);
     if (!row_ok || b >= nblk_padded) return;
     if (b >= nb) {
-      zero_block(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+      zero_block<N>(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
       return;
     }
     float xv[32];
@@ -490,6 +500,35 @@ hipError_t launch_prepare(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, 
     if (gamma) SHARQ_PREP(8, 16, true); else SHARQ_PREP(8, 16, false);
   }
 #undef SHARQ_PREP
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma, float eps,
+                               float* rms_scale, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+#define SHARQ_QUANT_ROWS(GG, QQ)                                                                                      \
+  do {                                                                                                               \
+    static int resident[64] = {};                                                                                    \
+    const uint64_t cap = resident_waves(reinterpret_cast<const void*>(&prepare_rms_rows_kernel<0, 0, GG, QQ>),      \
+                                        resident);                                                                   \
+    const uint64_t per_wave = ((uint64_t)T + cap - 1) / cap;                                                         \
+    const uint64_t waves = ((uint64_t)T + per_wave - 1) / per_wave;                                                  \
+    hipLaunchKernelGGL((prepare_rms_rows_kernel<0, 0, GG, QQ>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0,    \
+                       stream, x, ldx, gamma, (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales, nullptr,     \
+                       nullptr, nullptr);                                                                            \
+  } while (0)
+#define SHARQ_QUANT_RMS(GG)                                                                                          \
+  hipLaunchKernelGGL((prepare_rms_kernel<0, 0, GG>), dim3((unsigned)((T + kRmsRows - 1) / kRmsRows)), dim3(256), 0, \
+                     stream, x, ldx, gamma, (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales, nullptr,       \
+                     nullptr, nullptr)
+  if (K <= 2048) {
+    if (gamma) SHARQ_QUANT_ROWS(true, 1); else SHARQ_QUANT_ROWS(false, 1);
+  } else if (K <= 4096) {
+    if (gamma) SHARQ_QUANT_ROWS(true, 2); else SHARQ_QUANT_ROWS(false, 2);
+  } else {
+    if (gamma) SHARQ_QUANT_RMS(true); else SHARQ_QUANT_RMS(false);
+  }
+#undef SHARQ_QUANT_RMS
+#undef SHARQ_QUANT_ROWS
   return hipGetLastError();
 }
 

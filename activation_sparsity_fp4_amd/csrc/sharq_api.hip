@@ -355,6 +355,175 @@ int sharq_moe_combine(const float* y, int64_t P, int64_t H, const int32_t* pair_
   return hip_status(sharq::launch_moe_combine(y, P, H, pair_index, weights, T, k, out, out_bf16, stream));
 }
 
+int sharq_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, const int32_t* pair_index, const float* weights,
+                           int64_t T, int32_t k, float* out, uint16_t* out_bf16, hipStream_t stream) {
+  if (P < 0 || H <= 0 || H % 4 != 0 || T < 0 || k < 1 || k > 64) return SHARQ_EINVAL;
+  if (T >= ((int64_t)1 << 31) || T * (H / 4) >= ((int64_t)1 << 32) - 256) return SHARQ_EINVAL;  // 32-bit lane index
+  if (!out && !out_bf16) return SHARQ_EINVAL;  // nothing to write
+  if (T == 0) return SHARQ_OK;
+  if (!pair_index || !weights || (P > 0 && !y)) return SHARQ_EINVAL;
+  if ((y && !aligned16(y)) || (out && !aligned16(out)) || (out_bf16 && !aligned16(out_bf16)) ||
+      ((uintptr_t)pair_index & 3u) || ((uintptr_t)weights & 3u))
+    return SHARQ_EALIGN;
+  return hip_status(sharq::launch_moe_combine_bf16(y, P, H, pair_index, weights, T, k, out, out_bf16, stream));
+}
+
+int sharq_quantize_mxfp4_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma, float eps,
+                             float* rms_scale, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  const int rc = check_rows(T, K, ldx);
+  if (rc != SHARQ_OK) return rc;
+  if (!(eps > 0.0f) || !(eps < INFINITY)) return SHARQ_EINVAL;
+  if (K / 32 > 4096) return SHARQ_ENOTIMPL;  // the row-sum tree holds at most 4096 blocks
+  if (T == 0) return SHARQ_OK;
+  if (!x || !codes || !scales) return SHARQ_EINVAL;
+  if (!aligned16(x) || (gamma && !aligned16(gamma)) || (rms_scale && ((uintptr_t)rms_scale & 3u)) ||
+      !aligned16(codes) || !aligned16(scales))
+    return SHARQ_EALIGN;
+  return hip_status(sharq::launch_quantize_rms(x, T, K, ldx, gamma, eps, rms_scale, codes, scales, stream));
+}
+
+namespace {
+
+// Rows of a plain MXFP4 operand: a stage is one buffer view of 64 bytes a row,
+// whose offsets stay below 2^31.
+constexpr int64_t kMaxMxRows = (int64_t)1 << 25;
+
+int check_mx(int64_t rows, int64_t O, int64_t K) {
+  if (rows < 0 || O < 0 || K <= 0 || K % 32 != 0) return SHARQ_EINVAL;
+  if (rows >= kMaxMxRows || O >= kMaxMxRows || K >= ((int64_t)1 << 31)) return SHARQ_EINVAL;
+  return SHARQ_OK;
+}
+
+bool mx_null(const sharq::MxProduct& m) { return !m.a_codes || !m.a_scales || !m.w_codes || !m.w_scales; }
+bool mx_aligned(const sharq::MxProduct& m) {
+  return aligned16(m.a_codes) && aligned16(m.a_scales) && aligned16(m.w_codes) && aligned16(m.w_scales);
+}
+
+// Workgroups of a dense product's grid (32-row tiles at most below 33 rows).
+bool mx_grid_ok(int64_t T, int64_t O) {
+  return ((T + 127) / 128) * ((O + 255) / 256) * 16 <= kMaxGroupedTiles;  // 16: the largest K split
+}
+
+int check_workspace(const void* workspace, int64_t bytes) {
+  if (bytes < 0 || (bytes > 0 && !workspace)) return SHARQ_EINVAL;
+  return workspace && !aligned16(workspace) ? SHARQ_EALIGN : SHARQ_OK;
+}
+
+}  // namespace
+
+int64_t sharq_linear_mxfp4_workspace_bytes(int64_t T, int64_t O, int64_t K) {
+  if (check_mx(T, O, K) != SHARQ_OK || !mx_grid_ok(T, O)) return 0;
+  return sharq::mx_linear_workspace_bytes(T, O, K);
+}
+
+int sharq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                       const uint8_t* w_scales, int64_t T, int64_t O, int64_t K, void* y, int64_t ldy, int dtype,
+                       void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T, O, K};
+  int rc = check_mx(T, O, K);
+  if (rc != SHARQ_OK) return rc;
+  if (ldy < O || (dtype != SHARQ_F32 && dtype != SHARQ_BF16) || !mx_grid_ok(T, O)) return SHARQ_EINVAL;
+  if ((rc = check_workspace(workspace, workspace_bytes)) != SHARQ_OK) return rc;
+  if (T == 0 || O == 0) return SHARQ_OK;
+  if (mx_null(m) || !y) return SHARQ_EINVAL;
+  if (!mx_aligned(m) || !aligned16(y)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_mx_linear(m, y, ldy, dtype == SHARQ_BF16, workspace, workspace_bytes, stream));
+}
+
+int64_t sharq_linear_silu_mxfp4_workspace_bytes(int64_t T, int64_t I, int64_t K) {
+  if (I < 0 || I >= kMaxMxRows / 2) return 0;
+  return sharq_linear_mxfp4_workspace_bytes(T, 2 * I, K);
+}
+
+int sharq_linear_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                            const uint8_t* w_scales, int64_t T, int64_t I, int64_t K, uint8_t* h_codes,
+                            uint8_t* h_scales, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (I <= 0 || I % 32 != 0 || I >= kMaxMxRows / 2) return SHARQ_EINVAL;
+  const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T, 2 * I, K};
+  int rc = check_mx(T, 2 * I, K);
+  if (rc != SHARQ_OK) return rc;
+  if (!mx_grid_ok(T, 2 * I + 256)) return SHARQ_EINVAL;  // 256: a partial last h tile
+  if ((rc = check_workspace(workspace, workspace_bytes)) != SHARQ_OK) return rc;
+  if (T == 0) return SHARQ_OK;
+  if (mx_null(m) || !h_codes || !h_scales) return SHARQ_EINVAL;
+  if (!mx_aligned(m) || !aligned16(h_codes) || !aligned16(h_scales)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_mx_linear_silu(m, h_codes, h_scales, workspace, workspace_bytes, stream));
+}
+
+namespace {
+
+int check_mx_grouped(const sharq::MxProduct& m, const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
+                     int64_t P, int64_t tiles_n) {
+  const int rc = check_mx(m.rows, m.O, m.K);
+  if (rc != SHARQ_OK) return rc;
+  if (E < 1 || P < 0 || P >= ((int64_t)1 << 31) || (!a_rows && m.rows < P)) return SHARQ_EINVAL;
+  if (sharq::mx_grouped_workgroups(P, E, tiles_n) > kMaxGroupedTiles) return SHARQ_EINVAL;
+  if (P == 0 || m.O == 0) return SHARQ_OK;
+  if (mx_null(m) || !seg_offsets) return SHARQ_EINVAL;
+  if (!mx_aligned(m) || ((uintptr_t)seg_offsets & 3u) || ((uintptr_t)a_rows & 3u)) return SHARQ_EALIGN;
+  return SHARQ_OK;
+}
+
+}  // namespace
+
+int sharq_linear_grouped_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src, const int32_t* a_rows,
+                               const int32_t* seg_offsets, int32_t E, const uint8_t* w_codes, const uint8_t* w_scales,
+                               int64_t P, int64_t O, int64_t K, void* y, int dtype, hipStream_t stream) {
+  const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T_src, O, K};
+  if (dtype != SHARQ_F32 && dtype != SHARQ_BF16) return SHARQ_EINVAL;
+  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P, (O + 255) / 256);
+  if (rc != SHARQ_OK || P == 0 || O == 0) return rc;
+  if (!y) return SHARQ_EINVAL;
+  if (!aligned16(y)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_mx_grouped(m, a_rows, seg_offsets, E, P, y, dtype == SHARQ_BF16, stream));
+}
+
+int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src,
+                                    const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t P, int64_t I, int64_t K,
+                                    uint8_t* h_codes, uint8_t* h_scales, hipStream_t stream) {
+  if (I <= 0 || I % 32 != 0 || I >= kMaxMxRows / 2 || P >= kMaxMxRows) return SHARQ_EINVAL;
+  const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T_src, 2 * I, K};
+  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P, (I + 127) / 128);
+  if (rc != SHARQ_OK || P == 0) return rc;
+  if (!h_codes || !h_scales) return SHARQ_EINVAL;
+  if (!aligned16(h_codes) || !aligned16(h_scales)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_mx_grouped_silu(m, a_rows, seg_offsets, E, P, h_codes, h_scales, stream));
+}
+
+int64_t sharq_moe_route_workspace_bytes(int64_t T, int32_t E) {
+  if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > 1024) return 0;
+  return sharq::moe_route_workspace_bytes(T, E);
+}
+
+int sharq_moe_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t ldl, const float* bias, int32_t k,
+                    int score, int32_t groups, int32_t top_groups, int group_score, int renormalize, float scale,
+                    const int32_t* num_tokens, int32_t* expert, float* weight, int32_t* seg_offsets, int32_t* a_rows,
+                    int32_t* pair_index, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || k < 1 || k > E || ldl < E) return SHARQ_EINVAL;
+  if (dtype != SHARQ_F32 && dtype != SHARQ_BF16 && dtype != SHARQ_F16) return SHARQ_EINVAL;
+  if (score != SHARQ_SOFTMAX && score != SHARQ_SIGMOID) return SHARQ_EINVAL;
+  if (group_score != SHARQ_GROUP_MAX && group_score != SHARQ_GROUP_SUM2) return SHARQ_EINVAL;
+  if (groups < 1 || E % groups != 0 || top_groups < 1 || top_groups > groups || k > E / groups * top_groups)
+    return SHARQ_EINVAL;
+  if (!(fabsf(scale) < INFINITY)) return SHARQ_EINVAL;
+  if (T * k >= ((int64_t)1 << 31)) return SHARQ_EINVAL;  // 32-bit pairs
+  if (E > 1024 || k > 64) return SHARQ_ENOTIMPL;
+  int rc = check_workspace(workspace, workspace_bytes);
+  if (rc != SHARQ_OK) return rc;
+  if (workspace_bytes < sharq::moe_route_workspace_bytes(T, E)) return SHARQ_EINVAL;
+  if (!seg_offsets || (T > 0 && (!logits || !expert || !weight || !a_rows || !pair_index))) return SHARQ_EINVAL;
+  const uintptr_t item = dtype == SHARQ_F32 ? 3u : 1u;
+  if (((uintptr_t)logits & item) || ((uintptr_t)bias & 3u) || ((uintptr_t)num_tokens & 3u) ||
+      ((uintptr_t)expert & 3u) || ((uintptr_t)weight & 3u) || ((uintptr_t)seg_offsets & 3u) ||
+      ((uintptr_t)a_rows & 3u) || ((uintptr_t)pair_index & 3u))
+    return SHARQ_EALIGN;
+  const sharq::RouteArgs a{logits, dtype, T, ldl, E, k, bias, groups, top_groups, group_score == SHARQ_GROUP_SUM2,
+                           score == SHARQ_SIGMOID, renormalize != 0, scale, num_tokens, expert, weight, seg_offsets,
+                           a_rows, pair_index, static_cast<int32_t*>(workspace)};
+  return hip_status(sharq::launch_moe_route(a, stream));
+}
+
 namespace {
 
 // Shape checks of the layout conversions.

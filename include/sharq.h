@@ -79,6 +79,9 @@ typedef enum {
   SHARQ_ESCRATCH = -6      /* needs more scratch than SHARQ_SCRATCHFREE_MAX_BYTES */
 } sharq_status;
 
+/* Element types of the arguments that come in several. */
+enum { SHARQ_F32 = 0, SHARQ_BF16 = 1, SHARQ_F16 = 2 };
+
 /* Host. Static string describing a status code; never NULL. */
 SHARQ_API const char* sharq_status_string(int status);
 
@@ -492,6 +495,134 @@ SHARQ_API int sharq_linear_nvfp4(const uint8_t* bb_codes, const uint8_t* bb_scal
                        const uint8_t* w_scales, float w_tensor_scale,
                        int64_t T, int64_t O, int64_t K, float* y, int64_t ldy,
                        hipStream_t stream);
+
+/*
+ * Plain MXFP4 path: the dense product that the two-path GEMM decomposes, for
+ * layers that run without the decomposition (one activation operand, half the
+ * matrix work, the same weights).
+ *
+ * sharq_quantize_mxfp4_rms -- sharq_quantize_mxfp4 of the RMS-normed rows, the
+ * norm as in sharq_prepare_rms (same sums, same roundings):
+ *   x' = bf16_rne(fp32(x) * r) * gamma  (fp32; gamma may be NULL).
+ *  rms_scale  fp32 [T], written with r, or NULL.
+ *  codes, scales  u8 [G][T][64], [G][T][4].
+ * Requirements as sharq_prepare_rms (without the pattern).
+ */
+SHARQ_API int sharq_quantize_mxfp4_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma,
+                             float eps, float* rms_scale, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/*
+ * sharq_linear_mxfp4 -- Y[t][o] = sum_k deq(A)[t][k] * deq(W)[o][k].
+ *  a_codes u8 [G][T][64], a_scales u8 [G][T][4]; w_codes u8 [G][O][64],
+ *  w_scales u8 [G][O][4] (stage-major; the padding of a last, partial stage
+ *  must hold zeros, as every quantiser and packer here writes it);
+ *  y  [T][ldy] of type dtype: SHARQ_F32, or SHARQ_BF16 (the fp32 sum rounded
+ *     to nearest even); overwritten. Any ldy >= O.
+ *  workspace, workspace_bytes  device memory of at least
+ *     sharq_linear_mxfp4_workspace_bytes(T, O, K) bytes, 16-byte aligned, with
+ *     which K is split across workgroups where that is faster (few output
+ *     tiles, long K); contents need no initialisation and are overwritten.
+ *     With a smaller or NULL workspace K is not split. Calls that may overlap
+ *     in time need separate workspaces.
+ * Accumulation is fp32 in an order that depends on the shape (and on whether
+ * K was split) only, so calls are deterministic. Requires K % 32 == 0,
+ * T, O < 2^25, ceil(T/128) * ceil(O/256) <= 2^20.
+ */
+SHARQ_API int64_t sharq_linear_mxfp4_workspace_bytes(int64_t T, int64_t O, int64_t K);
+SHARQ_API int sharq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                       const uint8_t* w_scales, int64_t T, int64_t O, int64_t K, void* y, int64_t ldy, int dtype,
+                       void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * sharq_linear_silu_mxfp4 -- a fused gate|up projection on the plain path:
+ * sharq_linear_mxfp4 against a weight of I gate rows followed by I up rows,
+ * h = bf16(silu(Y[t][i]) * Y[t][I + i]) (as sharq_silu_mul), and h coded as
+ * sharq_quantize_mxfp4 codes it. Neither Y nor h passes through memory.
+ *  h_codes u8 [ceil(I/128)][T][64], h_scales u8 [ceil(I/128)][T][4].
+ *  workspace as for sharq_linear_mxfp4 (here
+ *  sharq_linear_silu_mxfp4_workspace_bytes(T, I, K) bytes).
+ * Bit-identical to sharq_linear_mxfp4 (T, 2 I, K; fp32; the same workspace or
+ * none) + sharq_silu_mul + sharq_quantize_mxfp4. Requires I % 32 == 0 and what
+ * sharq_linear_mxfp4 requires of (T, 2 I + 256, K).
+ */
+SHARQ_API int64_t sharq_linear_silu_mxfp4_workspace_bytes(int64_t T, int64_t I, int64_t K);
+SHARQ_API int sharq_linear_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                            const uint8_t* w_scales, int64_t T, int64_t I, int64_t K, uint8_t* h_codes,
+                            uint8_t* h_scales, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * sharq_linear_grouped_mxfp4, sharq_linear_grouped_silu_mxfp4 -- the two per
+ * expert segment, with the segments, the row gather and the per-expert weights
+ * of sharq_linear_grouped. Output row p is sorted pair p; rows of no segment
+ * (behind seg_offsets[E]) are not written.
+ *  a_codes u8 [G][T_src][64], a_scales u8 [G][T_src][4]; a_rows i32 [P] or
+ *  NULL; seg_offsets i32 [E+1]; w_codes u8 [E][G][O][64], w_scales
+ *  u8 [E][G][O][4] (O = 2 I for the fused form);
+ *  y [P][O] of type dtype; h_codes u8 [ceil(I/128)][P][64], h_scales.
+ * Malformed segment or gather contents are handled as sharq_linear_grouped
+ * does. Requires T_src, O < 2^25 (P < 2^25 for the fused form) and at most
+ * 2^24 workgroups: (ceil(P / rows) + E) * ceil(O / 256), rows = 32 for
+ * P <= 16 E, 64 for P <= 64 E, else 128.
+ */
+SHARQ_API int sharq_linear_grouped_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src,
+                               const int32_t* a_rows, const int32_t* seg_offsets, int32_t E, const uint8_t* w_codes,
+                               const uint8_t* w_scales, int64_t P, int64_t O, int64_t K, void* y, int dtype,
+                               hipStream_t stream);
+SHARQ_API int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src,
+                                    const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t P, int64_t I, int64_t K,
+                                    uint8_t* h_codes, uint8_t* h_scales, hipStream_t stream);
+
+/*
+ * sharq_moe_route -- router logits to the experts of each token and the
+ * dispatch plan of the grouped calls.
+ *  logits  [T][ldl] of type dtype (SHARQ_F32, SHARQ_BF16 or SHARQ_F16), the
+ *          first E of each row used. An expert whose logit is -inf or NaN is
+ *          never chosen; +inf counts as the largest finite fp32.
+ *  score   SHARQ_SOFTMAX (over the row's experts) or SHARQ_SIGMOID: s[e].
+ *  bias    fp32 [E] or NULL. Experts are ordered by s + bias (float64; a NaN
+ *          or -inf sum is never chosen), without a bias by the logit (both
+ *          scores are monotone in it). Equal ones go to the lower index.
+ *  groups, top_groups, group_score: with groups > 1 the E / groups
+ *          consecutive experts of a group stand or fall together: only the
+ *          top_groups groups with the largest score stay (equal ones: the
+ *          lower index). A group's score is its largest ordering value
+ *          (SHARQ_GROUP_MAX), or the sum of its two largest s + bias (s
+ *          without a bias; a missing second adds nothing; SHARQ_GROUP_SUM2).
+ *  num_tokens  i32 [1] on the device, or NULL (= T): rows from there on are
+ *          padding and choose nothing.
+ * Outputs:
+ *  expert  i32 [T][k], best first; -1 where fewer than k could be chosen.
+ *  weight  fp32 [T][k]: s (without the bias), divided by the sum over the
+ *          chosen if renormalize, times scale; float64 inside, one rounding.
+ *          0 in an empty slot.
+ *  seg_offsets i32 [E+1], a_rows i32 [T k]: the pairs (token, expert) sorted
+ *          by expert, tokens in order inside one; a_rows[p] is the token of
+ *          pair p, -1 behind the last pair.
+ *  pair_index  i32 [T][k]: the sorted place of each slot, -1 in an empty one
+ *          (what sharq_moe_combine reads).
+ *  workspace  at least sharq_moe_route_workspace_bytes(T, E) bytes, 16-byte
+ *          aligned (may be 0 and NULL for T <= 64); overwritten.
+ * T = 0 writes seg_offsets only. Requires 1 <= k <= E / groups * top_groups,
+ * E % groups == 0, T k < 2^31; E <= 1024 and k <= 64 (SHARQ_ENOTIMPL).
+ */
+enum { SHARQ_SOFTMAX = 0, SHARQ_SIGMOID = 1 };
+enum { SHARQ_GROUP_MAX = 0, SHARQ_GROUP_SUM2 = 1 };
+SHARQ_API int64_t sharq_moe_route_workspace_bytes(int64_t T, int32_t E);
+SHARQ_API int sharq_moe_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t ldl, const float* bias,
+                    int32_t k, int score, int32_t groups, int32_t top_groups, int group_score, int renormalize,
+                    float scale, const int32_t* num_tokens, int32_t* expert, float* weight, int32_t* seg_offsets,
+                    int32_t* a_rows, int32_t* pair_index, void* workspace, int64_t workspace_bytes,
+                    hipStream_t stream);
+
+/*
+ * sharq_moe_combine_bf16 -- sharq_moe_combine of bf16 rows y [P][H] (what
+ * sharq_linear_grouped_mxfp4 writes with SHARQ_BF16): half the bytes read, the
+ * same fp32 sum in slot order. out_bf16 16-byte aligned.
+ */
+SHARQ_API int sharq_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, const int32_t* pair_index,
+                           const float* weights, int64_t T, int32_t k, float* out, uint16_t* out_bf16,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }
