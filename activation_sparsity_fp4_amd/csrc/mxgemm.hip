@@ -29,11 +29,8 @@ namespace {
 
 // Workgroup tile of NWM x NWN waves, each WM x WN MFMA tiles of 32 x 32
 // (WM along the tokens), and the layout of one LDS stage: activation codes,
-// weight codes, weight scales, activation scales (padded to 64 rows, the width
-// of one buffer->LDS load). When the activation's scale runs do not split
-// evenly over the waves the spare instructions read nothing into a trash area
-// at the end, so that every wave issues the same number of loads per stage.
-// WGS workgroups share a CU (bounded by the LDS and by the registers).
+// weight codes, and a KB for each operand's scales. WGS workgroups share a CU
+// (bounded by the LDS and by the registers).
 template <int WM_, int WN_, int NWM_, int NWN_, int RING_, int WGS_>
 struct MxTile {
   static constexpr int WM = WM_, WN = WN_, NWM = NWM_, NWN = NWN_;
@@ -42,16 +39,13 @@ struct MxTile {
   static constexpr int kOffA = 0;
   static constexpr int kOffW = BM * kRowBytes;
   static constexpr int kOffSW = kOffW + BN * kRowBytes;
-  static constexpr int kOffSA = kOffSW + BN * 4;
+  static constexpr int kOffSA = kOffSW + 1024;
+  static constexpr int kStage = kOffSA + 1024;
   static constexpr int kAChunks = BM / 16 / kWaves;
   static constexpr int kWChunks = BN / 16 / kWaves;
-  static constexpr int kARuns = (BM + 63) / 64;
-  static constexpr int kALoads = (kARuns + kWaves - 1) / kWaves;
-  static constexpr int kWLoads = BN / 64 / kWaves;
-  static constexpr int kLoads = kAChunks + kWChunks + kALoads + kWLoads;
-  static constexpr int kStage = kOffSA + 256 * kWaves * kALoads;
+  static constexpr int kCodeLoads = kAChunks + kWChunks;  // of a wave in a stage
   static_assert(kAChunks * 16 * kWaves == BM && kWChunks * 16 * kWaves == BN, "whole 1 KB chunks per wave");
-  static_assert(kWLoads * 64 * kWaves == BN, "whole scale runs per wave");
+  static constexpr int kHalf = WM * WN;  // MFMAs of half an iteration, a slot each
   static constexpr int kRing = RING_;
   static constexpr int kWavesPerSimd = (WGS_ * kWaves + 3) / 4;
   static_assert(kRing >= 2 && WGS_ * kRing * kStage <= kLdsBytes, "ring");
@@ -61,7 +55,6 @@ struct MxTile {
 using Mx32 = MxTile<1, 4, 1, 2, 3, 2>;
 using Mx64 = MxTile<2, 4, 1, 2, 3, 2>;
 using Mx128 = MxTile<2, 4, 2, 2, 3, 2>;
-using Mx256 = MxTile<4, 4, 2, 2, 4, 1>;
 
 struct MxOperands {
   const uint8_t* a_codes;   // [G][rows][64]
@@ -72,6 +65,16 @@ struct MxOperands {
   int nsteps;
 };
 
+// Scale loads of a wave in a stage, 16 bytes a lane: even waves the weight's
+// 256 dwords, odd waves the activation's (waves beyond the second repeat a
+// load, the same bytes to the same place, so that all waves count alike). When
+// rows are gathered: the weight's, and one 64-row run of the activation's with
+// a dword a lane. (Into LDS, a dword a lane holds the CU's load path for 32
+// cycles, 16 bytes a lane for 16. 16 bytes partly outside the view read zeros
+// per dword.)
+template <class C, bool kGather>
+constexpr int kLoads = C::kCodeLoads + (kGather ? 2 : 1);
+
 template <class C>
 struct MxFrags {
   v8i a[C::WM], w[C::WN];
@@ -81,36 +84,60 @@ struct MxScales {
   uint32_t a[C::WM], w[C::WN];
 };
 
-// One LDS read of the schedule: item R < WM + WN is a fragment of sub-step
-// SUB; the next WM + WN items (SUB = 0 only) are the scale dwords. The scale
-// dword of a row holds the bytes of the stage's 4 blocks; shifted right by
-// 8 (lane / 32), byte 0 (sub-step 0) and byte 2 (sub-step 1) are the blocks of
-// the lane's K half.
+// LDS reads in the order of their use: for sub-step 0 the stage's scale dwords
+// (two rows to an item), then the fragments; for sub-step 1 the fragments. The
+// scale dword of a row holds the bytes of the stage's 4 blocks; shifted right
+// by 8 (lane / 32), byte 0 (sub-step 0) and byte 2 (sub-step 1) are the blocks
+// of the lane's K half.
+template <class C, int SUB>
+constexpr int kScaleItems = SUB == 0 ? (C::WM + 1) / 2 + C::WN / 2 : 0;
+template <class C, int SUB>
+constexpr int kReadItems = kScaleItems<C, SUB> + C::WM + C::WN;
+
+// LDS reads of a slot: as many as finish the half's reads in the first 5/8 of
+// its slots, so that the other MFMAs cover the latency of the last ones.
+template <class C>
+constexpr int kReadsPerSlot = (kReadItems<C, 0> + C::kHalf * 5 / 8 - 1) / (C::kHalf * 5 / 8);
+
 template <class C, int SUB, int R>
 __device__ __forceinline__ void mx_read(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
                                         int lh) {
-  constexpr int kF = C::WM + C::WN;
-  if constexpr (R < C::WM) {
-    f.a[R] = frag(st + C::kOffA + swz(32 * C::WM * wm + 32 * R + lr, 2 * SUB + lh));
-  } else if constexpr (R < kF) {
-    constexpr int j = R - C::WM;
+  constexpr int kSA = (C::WM + 1) / 2, kS = kScaleItems<C, SUB>;
+  if constexpr (R < kS && R < kSA) {
+    const uint8_t* p = st + C::kOffSA + 4 * (32 * C::WM * wm + 64 * R + lr);
+    c.a[2 * R] = *reinterpret_cast<const uint32_t*>(p);
+    if constexpr (2 * R + 1 < C::WM) c.a[2 * R + 1] = *reinterpret_cast<const uint32_t*>(p + 128);
+  } else if constexpr (R < kS) {
+    constexpr int j = 2 * (R - kSA);
+    const uint8_t* p = st + C::kOffSW + 4 * (32 * C::WN * wn + 32 * j + lr);
+    c.w[j] = *reinterpret_cast<const uint32_t*>(p);
+    c.w[j + 1] = *reinterpret_cast<const uint32_t*>(p + 128);
+  } else if constexpr (R < kS + C::WM) {
+    constexpr int i = R - kS;
+    f.a[i] = frag(st + C::kOffA + swz(32 * C::WM * wm + 32 * i + lr, 2 * SUB + lh));
+  } else if constexpr (R < kS + C::WM + C::WN) {
+    constexpr int j = R - kS - C::WM;
     f.w[j] = frag(st + C::kOffW + swz(32 * C::WN * wn + 32 * j + lr, 2 * SUB + lh));
-  } else if constexpr (SUB == 0 && R < kF + C::WM) {
-    constexpr int i = R - kF;
-    c.a[i] = *reinterpret_cast<const uint32_t*>(st + C::kOffSA + 4 * (32 * C::WM * wm + 32 * i + lr)) >> (8 * lh);
-  } else if constexpr (SUB == 0 && R < 2 * kF) {
-    constexpr int j = R - kF - C::WM;
-    c.w[j] = *reinterpret_cast<const uint32_t*>(st + C::kOffSW + 4 * (32 * C::WN * wn + 32 * j + lr)) >> (8 * lh);
   }
 }
 
-template <class C, int R = 0>
-__device__ __forceinline__ void mx_read_first(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
+template <class C, int SUB, int R, int END>
+__device__ __forceinline__ void mx_read_range(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
                                               int lh) {
-  if constexpr (R < 2 * (C::WM + C::WN)) {
-    mx_read<C, 0, R>(st, f, c, wm, wn, lr, lh);
-    mx_read_first<C, R + 1>(st, f, c, wm, wn, lr, lh);
+  if constexpr (R < END && R < kReadItems<C, SUB>) {
+    mx_read<C, SUB, R>(st, f, c, wm, wn, lr, lh);
+    mx_read_range<C, SUB, R + 1, END>(st, f, c, wm, wn, lr, lh);
   }
+}
+
+// The shift of the scale dwords, kept where it stands (as an ordinary shift the
+// compiler moves it behind the loop's edge, where it waits for every LDS read).
+template <class C>
+__device__ __forceinline__ void mx_shift_scales(MxScales<C>& c, uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < C::WM; ++i) asm volatile("v_lshrrev_b32 %0, %1, %0" : "+v"(c.a[i]) : "v"(bits));
+#pragma unroll
+  for (int j = 0; j < C::WN; ++j) asm volatile("v_lshrrev_b32 %0, %1, %0" : "+v"(c.w[j]) : "v"(bits));
 }
 
 // MFMA number M of a sub-step. kSkip: row blocks from `active` on hold no
@@ -124,92 +151,121 @@ __device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, const MxScales<C>& 
                                                                 (int)c.w[j], 2 * SUB, (int)c.a[i]);
 }
 
-template <class C>
-struct MxLoader {
-  const uint8_t *a_codes, *w_codes, *a_scales, *w_scales;  // base of the next stage to load
-  uint32_t a_off[C::kAChunks];  // byte offset of this lane's A code chunk inside a stage, kOOB if absent
-  uint32_t w_off[C::kWChunks];
-  uint32_t sw_off[C::kWLoads];  // this lane's scale dword
-  uint32_t sa_off[C::kALoads];
-  int wave;
-  int left;  // stages not yet issued; batches past the last one read nothing
-  uint32_t a_rows, w_rows;
+// Buffer loads into LDS as in gemm_common.h, the LDS address a sum formed in
+// M0 itself: base + the bytes that the template names.
+template <int BYTES>
+__device__ __forceinline__ void load_lds16(i32x4 rsrc, uint32_t voff, uint32_t base) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(base), "n"(BYTES) : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t base, uint32_t bytes) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(base), "s"(bytes) : "memory", "m0", "scc");
+}
 
-  struct Dest {
-    uint32_t base;
-    i32x4 a, w, sa, sw;
-  };
-  // Buffer views of the next stage and its LDS slot; moves on to the stage after.
-  __device__ __forceinline__ Dest next(uint8_t* st) {
-    const uint32_t na = left > 0 ? a_rows : 0, nw = left > 0 ? w_rows : 0;
-    Dest d;
-    d.base = lds_offset(st);
-    d.a = make_rsrc(a_codes, (int64_t)na * kRowBytes);
-    d.w = make_rsrc(w_codes, (int64_t)nw * kRowBytes);
-    d.sa = make_rsrc(a_scales, (int64_t)na * 4);
-    d.sw = make_rsrc(w_scales, (int64_t)nw * 4);
-    --left;
-    a_codes += (int64_t)a_rows * kRowBytes;
-    w_codes += (int64_t)w_rows * kRowBytes;
-    a_scales += (int64_t)a_rows * 4;
-    w_scales += (int64_t)w_rows * 4;
-    return d;
+// One operand array: the buffer view of the stage to load next.
+struct MxView {
+  i32x4 r;
+  uint32_t stage_bytes;
+  __device__ __forceinline__ void start(const uint8_t* base, int64_t bytes, int stage) {
+    stage_bytes = (uint32_t)bytes;
+    r = make_rsrc(base + (int64_t)stage * bytes, bytes);
   }
-
-  template <int J>
-  __device__ __forceinline__ void issue(const Dest& d) const {
-    if constexpr (J < C::kAChunks) {
-      buffer_to_lds16(d.a, a_off[J], d.base + C::kOffA + 1024 * (wave + C::kWaves * J));
-    } else if constexpr (J < C::kAChunks + C::kWChunks) {
-      constexpr int j = J - C::kAChunks;
-      buffer_to_lds16(d.w, w_off[j], d.base + C::kOffW + 1024 * (wave + C::kWaves * j));
-    } else if constexpr (J < C::kAChunks + C::kWChunks + C::kWLoads) {
-      constexpr int i = J - C::kAChunks - C::kWChunks;
-      buffer_to_lds4(d.sw, sw_off[i], d.base + C::kOffSW + 256 * (wave + C::kWaves * i));
-    } else if constexpr (J < C::kLoads) {
-      constexpr int i = J - C::kAChunks - C::kWChunks - C::kWLoads;
-      buffer_to_lds4(d.sa, sa_off[i], d.base + C::kOffSA + 256 * (wave + C::kWaves * i));
-    }
-  }
-  template <int J = 0>
-  __device__ __forceinline__ void issue_all(const Dest& d) const {
-    if constexpr (J < C::kLoads) {
-      issue<J>(d);
-      issue_all<J + 1>(d);
-    }
+  // On to the next stage; without one, to a view of nothing.
+  __device__ __forceinline__ void advance(bool live) {
+    const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + stage_bytes;
+    r[0] = (int)(uint32_t)at;
+    r[1] = (int)(uint32_t)(at >> 32);
+    r[2] = live ? (int)stage_bytes : 0;
   }
 };
 
-// First half of an iteration: the sub-step 0 MFMAs of the stage, each followed
-// by one fragment read of its sub-step 1.
+// The loads of a wave. Every array's view moves on right behind its last load
+// of a stage, so that the scalar work is spread between the MFMAs too.
+template <class C, bool kGather>
+struct MxLoader {
+  MxView a, w, s, g;            // codes; the wave's 16-byte scale load; gathered activation scales
+  uint32_t a_off[C::kAChunks];  // byte offset of this lane's A code chunk inside a stage, kOOB if absent
+  uint32_t w_off[C::kWChunks];
+  uint32_t s_off, g_off;        // this lane's scale dwords
+  uint32_t wave_base;           // 1024 * wave: the wave's chunk inside a stage
+  uint32_t s_lds, g_lds;        // where its scales go inside a stage
+  uint32_t ring, at;            // LDS address of the ring; offset of the slot to fill
+  int left;                     // stages not yet issued; batches past the last one read nothing
+
+  template <int J>
+  __device__ __forceinline__ void issue() {
+    constexpr int kN = kLoads<C, kGather>;
+    if constexpr (J < C::kAChunks) {
+      load_lds16<C::kOffA + 1024 * C::kWaves * J>(a.r, a_off[J], ring + at + wave_base);
+      if constexpr (J == C::kAChunks - 1) a.advance(--left > 0);
+    } else if constexpr (J < C::kCodeLoads) {
+      constexpr int j = J - C::kAChunks;
+      load_lds16<C::kOffW + 1024 * C::kWaves * j>(w.r, w_off[j], ring + at + wave_base);
+      if constexpr (J == C::kCodeLoads - 1) w.advance(left > 0);
+    } else if constexpr (J == C::kCodeLoads) {
+      load_lds16<0>(s.r, s_off, ring + at + s_lds);
+      s.advance(left > 0);
+    } else if constexpr (J < kN) {
+      load_lds4(g.r, g_off, ring + at, g_lds);
+      g.advance(left > 0);
+    }
+    if constexpr (J == kN - 1) at = at + C::kStage == C::kRing * C::kStage ? 0 : at + C::kStage;
+  }
+  template <int J, int END>
+  __device__ __forceinline__ void issue_range() {
+    if constexpr (J < END) {
+      issue<J>();
+      issue_range<J + 1, END>();
+    }
+  }
+  // Loads of slots [0, SLOT) of the 2 kHalf slots over which a stage's are spread.
+  template <int SLOT>
+  static constexpr int kBefore = (SLOT * kLoads<C, kGather> + 2 * C::kHalf - 1) / (2 * C::kHalf);
+  template <int FROM, int TO>
+  __device__ __forceinline__ void issue_slots() {
+    issue_range<kBefore<FROM>, kBefore<TO>>();
+  }
+};
+
+// An iteration is two halves of one MFMA a slot, the other work threaded
+// between the MFMAs:
+//   first half: the sub-step 0 MFMAs of stage s, the fragment reads of its
+//     sub-step 1;
+//   wait for stage s + 1 and barrier: stage s is in registers in every wave,
+//     so its LDS slot is free;
+//   second half: the sub-step 1 MFMAs, the scale and fragment reads of stage
+//     s + 1.
+// The loads of stage s + ring go into the freed slot, spread evenly over the
+// second half and the first half of the next iteration: the waves of a barrier
+// that issue theirs in a burst queue up at the CU's one load path (16 cycles a
+// KB), and an MFMA behind a queued load waits with it.
 template <class C, int M, bool kSkip>
 __device__ __forceinline__ void mx_first_half(const MxFrags<C>& f0, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
-                                              const uint8_t* cur, MxFrags<C>& f1, MxScales<C>& unused, int wm, int wn,
-                                              int lr, int lh, int active) {
-  constexpr int kF = C::WM + C::WN, kM = C::WM * C::WN;
-  if constexpr (M < kM || M < kF) {
-    if constexpr (M < kM) mx_mfma<C, 0, M, kSkip>(f0, c, acc, active);
-    mx_read<C, 1, M>(cur, f1, unused, wm, wn, lr, lh);
+                                              MxLoader<C, kSkip>& ld, const uint8_t* cur,
+                                              MxFrags<C>& f1, MxScales<C>& unused, int wm, int wn, int lr, int lh,
+                                              int active) {
+  if constexpr (M < C::kHalf) {
+    mx_mfma<C, 0, M, kSkip>(f0, c, acc, active);
+    mx_read_range<C, 1, M * kReadsPerSlot<C>, (M + 1) * kReadsPerSlot<C>>(cur, f1, unused, wm, wn, lr, lh);
+    ld.template issue_slots<C::kHalf + M, C::kHalf + M + 1>();
     __builtin_amdgcn_sched_barrier(0);
-    mx_first_half<C, M + 1, kSkip>(f0, c, acc, cur, f1, unused, wm, wn, lr, lh, active);
+    mx_first_half<C, M + 1, kSkip>(f0, c, acc, ld, cur, f1, unused, wm, wn, lr, lh, active);
   }
 }
 
-// Second half, after the wait for the next stage and the barrier that frees
-// this stage's slot: the sub-step 1 MFMAs, each followed by one load of the
-// stage that goes into the freed slot and one LDS read of the next stage.
 template <class C, int M, bool kSkip>
 __device__ __forceinline__ void mx_second_half(const MxFrags<C>& f1, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
-                                               const MxLoader<C>& ld, const typename MxLoader<C>::Dest& d,
-                                               const uint8_t* next, MxFrags<C>& f0, MxScales<C>& cn, int wm, int wn,
-                                               int lr, int lh, int active) {
-  constexpr int kM = C::WM * C::WN, kItems = 2 * (C::WM + C::WN);
-  if constexpr (M < kM || M < C::kLoads || M < kItems) {
-    if constexpr (M < kM) mx_mfma<C, 1, M, kSkip>(f1, c, acc, active);
-    ld.template issue<M>(d);
-    mx_read<C, 0, M>(next, f0, cn, wm, wn, lr, lh);
+                                               MxLoader<C, kSkip>& ld, const uint8_t* next,
+                                               MxFrags<C>& f0, MxScales<C>& cn, int wm, int wn, int lr, int lh,
+                                               int active) {
+  if constexpr (M < C::kHalf) {
+    mx_mfma<C, 1, M, kSkip>(f1, c, acc, active);
+    mx_read_range<C, 0, M * kReadsPerSlot<C>, (M + 1) * kReadsPerSlot<C>>(next, f0, cn, wm, wn, lr, lh);
+    if constexpr (M == C::kHalf - 1) mx_shift_scales<C>(cn, 8 * lh);
+    ld.template issue_slots<M, M + 1>();
     __builtin_amdgcn_sched_barrier(0);
-    mx_second_half<C, M + 1, kSkip>(f1, c, acc, ld, d, next, f0, cn, wm, wn, lr, lh, active);
+    mx_second_half<C, M + 1, kSkip>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh, active);
   }
 }
 
@@ -228,15 +284,19 @@ __device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows
       : tr.rows_valid <= first_row ? 0
       : (int)min<int64_t>((tr.rows_valid - first_row + 31) / 32, C::WM));
 
-  MxLoader<C> ld;
-  ld.wave = wave;
+  MxLoader<C, kSkip> ld;
+  constexpr int kARuns = (C::BM + 63) / 64;
+  const bool act_scales = !kSkip && (wave & 1);
   ld.left = s_end - s_begin;
-  ld.a_rows = (uint32_t)op.rows;
-  ld.w_rows = (uint32_t)op.O;
-  ld.a_codes = op.a_codes + (int64_t)s_begin * op.rows * kRowBytes;
-  ld.w_codes = op.w_codes + (int64_t)s_begin * op.O * kRowBytes;
-  ld.a_scales = op.a_scales + (int64_t)s_begin * op.rows * 4;
-  ld.w_scales = op.w_scales + (int64_t)s_begin * op.O * 4;
+  ld.a.start(op.a_codes, op.rows * kRowBytes, s_begin);
+  ld.w.start(op.w_codes, op.O * kRowBytes, s_begin);
+  ld.s.start(act_scales ? op.a_scales : op.w_scales, (act_scales ? op.rows : op.O) * 4, s_begin);
+  if (kSkip) ld.g.start(op.a_scales, op.rows * 4, s_begin);
+  ld.wave_base = 1024 * wave;
+  ld.s_lds = act_scales ? C::kOffSA : C::kOffSW;
+  ld.g_lds = C::kOffSA + 256 * (wave % kARuns);
+  ld.ring = lds_offset(ring);
+  ld.at = 0;
   // A lane fills a fixed LDS chunk; it reads the global chunk that belongs there after the swizzle.
 #pragma unroll
   for (int j = 0; j < C::kAChunks; ++j) {
@@ -250,43 +310,45 @@ __device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows
     const int64_t o = tc.w_row(row);
     ld.w_off[j] = o < op.O ? (uint32_t)(o * kRowBytes + ((lane & 3) ^ swz_part(row)) * 16) : kOOB;
   }
-#pragma unroll
-  for (int i = 0; i < C::kWLoads; ++i) {
-    const int64_t o = tc.w_row(64 * (wave + C::kWaves * i) + lane);
-    ld.sw_off[i] = o < op.O ? (uint32_t)(o * 4) : kOOB;
+  ld.s_off = ld.g_off = kOOB;
+  if (!act_scales) {
+    const int64_t o = tc.w_row(4 * lane);  // four rows of one 64-row block
+    if (o < op.O) ld.s_off = (uint32_t)(o * 4);
+  } else if (4 * lane < C::BM && tr.m0 + 4 * lane < op.rows) {
+    ld.s_off = (uint32_t)((tr.m0 + 4 * lane) * 4);
   }
-#pragma unroll
-  for (int i = 0; i < C::kALoads; ++i) {
-    const int q = wave + C::kWaves * i;  // a spare instruction (q >= kARuns) reads nothing
-    const int64_t src = q < C::kARuns ? tr.src(64 * q + lane) : -1;
-    ld.sa_off[i] = src >= 0 ? (uint32_t)(src * 4) : kOOB;
+  if (kSkip) {
+    const int64_t src = tr.src(64 * (wave % kARuns) + lane);
+    if (src >= 0) ld.g_off = (uint32_t)(src * 4);
   }
 
+  // The first ring of stages; the last one's first-half loads follow in the loop.
+  constexpr int kN = kLoads<C, kSkip>;
 #pragma unroll
-  for (int b = 0; b < C::kRing; ++b) ld.issue_all(ld.next(ring + b * C::kStage));
-  wait_vmcnt<(C::kRing - 1) * C::kLoads>();  // the first batch landed
+  for (int b = 0; b + 1 < C::kRing; ++b) ld.template issue_range<0, kN>();
+  ld.template issue_slots<0, C::kHalf>();
+  wait_vmcnt<(C::kRing - 2) * kN + MxLoader<C, kSkip>::template kBefore<C::kHalf>>();  // the first batch landed
   ring_barrier();
   MxFrags<C> f0, f1;
   MxScales<C> c, cn;
-  mx_read_first<C>(ring, f0, c, wm, wn, lr, lh);
-  int slot = 0;
+  mx_read_range<C, 0, 0, kReadItems<C, 0>>(ring, f0, c, wm, wn, lr, lh);
+  mx_shift_scales<C>(c, 8 * lh);
+  const uint8_t* cur = ring;
 #pragma unroll 1
   for (int s = s_begin; s < s_end; ++s) {
-    uint8_t* cur = ring + slot * C::kStage;
-    slot = slot + 1 == C::kRing ? 0 : slot + 1;
-    const uint8_t* next = ring + slot * C::kStage;
+    const uint8_t* next = cur == ring + (C::kRing - 1) * C::kStage ? ring : cur + C::kStage;
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
-    mx_first_half<C, 0, kSkip>(f0, c, acc, cur, f1, cn, wm, wn, lr, lh, active);
+    mx_first_half<C, 0, kSkip>(f0, c, acc, ld, cur, f1, cn, wm, wn, lr, lh, active);
     __builtin_amdgcn_s_setprio(0);
-    wait_vmcnt<(C::kRing - 2) * C::kLoads>();  // the next stage landed; later batches may be in flight
+    wait_vmcnt<(C::kRing - 2) * kN>();  // the next stage landed; later batches may be in flight
     ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const typename MxLoader<C>::Dest d = ld.next(cur);
     __builtin_amdgcn_s_setprio(1);
-    mx_second_half<C, 0, kSkip>(f1, c, acc, ld, d, next, f0, cn, wm, wn, lr, lh, active);
+    mx_second_half<C, 0, kSkip>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh, active);
     __builtin_amdgcn_s_setprio(0);
     c = cn;
+    cur = next;
   }
   wait_vmcnt<0>();  // the trailing batches, before the LDS is used again
 }
@@ -607,13 +669,9 @@ MxOperands mx_operands(const MxProduct& p) {
   return MxOperands{p.a_codes, p.a_scales, p.w_codes, p.w_scales, p.rows, p.O, (int)((p.K + 127) / 128)};
 }
 
-// Row tile of a dense product: 0 Mx32, 1 Mx64, 2 Mx128, 3 Mx256.
-int mx_row_tile(int64_t T, int64_t O) {
-  if (T <= 32) return 0;
-  if (T <= 64) return 1;
-  return (T + 255) / 256 * ((O + 255) / 256) >= 256 ? 3 : 2;
-}
-int64_t mx_tile_rows(int tile) { return tile == 0 ? 32 : tile == 1 ? 64 : tile == 2 ? 128 : 256; }
+// Row tile of a dense product: 0 Mx32, 1 Mx64, 2 Mx128.
+int mx_row_tile(int64_t T) { return T <= 32 ? 0 : T <= 64 ? 1 : 2; }
+int64_t mx_tile_rows(int tile) { return tile == 0 ? 32 : tile == 1 ? 64 : 128; }
 
 struct MxPlan {
   int tile, S;
@@ -621,11 +679,11 @@ struct MxPlan {
 };
 
 MxPlan mx_plan(int64_t T, int64_t O, int64_t K, bool may_split) {
-  MxPlan p{mx_row_tile(T, O), 1, 0, 0};
+  MxPlan p{mx_row_tile(T), 1, 0, 0};
   const int64_t bm = mx_tile_rows(p.tile);
   p.tiles_m = (int)((T + bm - 1) / bm);
   p.tiles_total = p.tiles_m * (int)((O + 255) / 256);
-  if (!may_split || p.tile == 3) return p;
+  if (!may_split) return p;
   const int64_t nsteps = (K + 127) / 128;
   const int64_t s_max = nsteps / 4 < kMxMaxSplits ? nsteps / 4 : kMxMaxSplits;
   double best = 0;
@@ -654,8 +712,7 @@ void launch_mx_store(const MxPlan& p, const MxOperands& op, Out* y, int64_t ldy,
                      wide, p.tiles_m, p.tiles_total)
   if (p.tile == 0) SHARQ_MX(Mx32);
   else if (p.tile == 1) SHARQ_MX(Mx64);
-  else if (p.tile == 2) SHARQ_MX(Mx128);
-  else SHARQ_MX(Mx256);
+  else SHARQ_MX(Mx128);
 #undef SHARQ_MX
 }
 
@@ -730,8 +787,7 @@ hipError_t launch_mx_linear_silu(const MxProduct& m, uint8_t* h_codes, uint8_t* 
                      p.tiles_total)
   if (p.tile == 0) SHARQ_MX(Mx32);
   else if (p.tile == 1) SHARQ_MX(Mx64);
-  else if (p.tile == 2) SHARQ_MX(Mx128);
-  else SHARQ_MX(Mx256);
+  else SHARQ_MX(Mx128);
 #undef SHARQ_MX
   return hipGetLastError();
 }
