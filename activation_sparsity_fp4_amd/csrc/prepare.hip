@@ -28,38 +28,28 @@
 namespace sharq {
 
 // Selection, quantisation and the stores of one block of x'. kLowBits: x'
-// may carry more than bf16's 8 significant bits (a product with gamma). N = 0
-// is the plain coding of the block: no mask, no residual.
+// may carry more than bf16's 8 significant bits (a product with gamma).
 template <int N, int M, bool kLowBits>
 __device__ __forceinline__ void prepare_store(const float (&xv)[32], uint32_t t, uint32_t b,
                                               uint32_t blocks_per_row, uint32_t rows,
                                               uint8_t* __restrict__ bb_codes, uint8_t* __restrict__ bb_scales,
                                               uint8_t* __restrict__ res_codes, uint8_t* __restrict__ res_scales,
                                               uint8_t* __restrict__ mask_out) {
-  if constexpr (N == 0) {
-    const uint32_t e = e8m0_from_amax_bits(amax_bits32(xv));
-    *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = quantize32(xv, scale_from_e8m0(e));
-    bb_scales[scale_index(t, b, rows)] = (uint8_t)e;
-  } else {
-    const PreparedBlock pb = prepare_block<N, M, kLowBits>(xv);
-    *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = pb.c_bb;
-    *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = pb.c_rs;
-    bb_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_bb;
-    res_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_rs;
-    if (mask_out) reinterpret_cast<uint32_t*>(mask_out)[(int64_t)t * blocks_per_row + b] = pb.keep;
-  }
+  const PreparedBlock pb = prepare_block<N, M, kLowBits>(xv);
+  *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = pb.c_bb;
+  *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = pb.c_rs;
+  bb_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_bb;
+  res_scales[scale_index(t, b, rows)] = (uint8_t)pb.e_rs;
+  if (mask_out) reinterpret_cast<uint32_t*>(mask_out)[(int64_t)t * blocks_per_row + b] = pb.keep;
 }
 
-template <int N>
 __device__ __forceinline__ void zero_block(uint32_t t, uint32_t b, uint32_t rows, uint8_t* __restrict__ bb_codes,
                                            uint8_t* __restrict__ bb_scales, uint8_t* __restrict__ res_codes,
                                            uint8_t* __restrict__ res_scales) {
   *reinterpret_cast<uint4*>(bb_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
   bb_scales[scale_index(t, b, rows)] = 0;
-  if constexpr (N != 0) {
-    *reinterpret_cast<uint4*>(res_codes + code_offset(t, b, rows)) = make_uint4(0, 0, 0, 0);
-    res_scales[scale_index(t, b, rows)] = 0;
-  }
+  res_scales[scale_index(t, b, rows)] = 0;
 }
 
 // The whole operator without the norm: x' = x (times gamma when given).
@@ -106,7 +96,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(
       prepare_store<N, M, kGamma>(xv, lb.t, lb.b, blocks_per_row, rows, bb_codes, bb_scales, res_codes,
                                   res_scales, mask_out);
     } else if (lb.row_ok) {
-      zero_block<N>(lb.t, lb.b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+      zero_block(lb.t, lb.b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
     }
     item = next;
     lb = nb;
@@ -193,7 +183,7 @@ __global__ __launch_bounds__(256) void prepare_rms_rows_kernel(
       root = q == 0 ? chunk : root + chunk;
     }
     const float r = (float)(1.0 / sqrt(root / (double)K + (double)eps));
-    if (lane == 0 && (N != 0 || r_out)) r_out[t] = r;
+    if (lane == 0) r_out[t] = r;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const uint32_t b = lane + 64 * q;
@@ -208,7 +198,7 @@ __global__ __launch_bounds__(256) void prepare_rms_rows_kernel(
         }
         prepare_store<N, M, kGamma>(xv, t, b, nb, rows, bb_codes, bb_scales, res_codes, res_scales, mask_out);
       } else if (b < nblk_padded) {
-        zero_block<N>(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+        zero_block(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
       }
     }
     t = next;
@@ -334,7 +324,7 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
       const float r = (float)(1.0 / sqrt(root / (double)K + (double)eps));
       r_row[wave] = r;
       const uint32_t tw = blockIdx.x * kRmsRows + wave;
-      if (tw < rows && (N != 0 || r_out)) r_out[tw] = r;
+      if (tw < rows) r_out[tw] = r;
     }
   }
   __syncthreads();
@@ -345,7 +335,7 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
     const uint32_t b = chunk_block(c);
     if (!row_ok || b >= nblk_padded) return;
     if (b >= nb) {
-      zero_block<N>(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
+      zero_block(t, b, rows, bb_codes, bb_scales, res_codes, res_scales);  // partial last stage
       return;
     }
     float xv[32];
@@ -367,6 +357,85 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
     uint4 raw[4];
     load_chunk(c, raw);
     emit(c, raw);
+  }
+}
+
+// Plain MXFP4 coding of RMS-normed rows: r as in prepare_rms_kernel, bit for
+// bit, then x' = bf16(x * r) (times gamma when given), amax, scale, codes.
+// One workgroup per row, a 32-entry block per thread and pass (blockDim is 64,
+// 128 or 256, a power of two, so that 64-lane xor trees over consecutive
+// blocks are the levels of the pairwise tree; addition commutes, so every lane
+// ends with the tree's root). The wave roots meet in LDS and every wave
+// finishes the tree on its own: one barrier. A thread's first kHold blocks
+// stay in registers between the sum and the coding, later ones (K > 16384) are
+// read again. HBM-bound for many rows (2 bytes read and 0.53 written an
+// entry); for a few rows one round trip to memory and the 32 dependent float64
+// additions of a block.
+template <bool kGamma, int kHold>
+__global__ __launch_bounds__(256) void quantize_rms_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                           const uint16_t* __restrict__ gamma, uint32_t K,
+                                                           uint32_t rows, float eps, float* __restrict__ r_out,
+                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ double part[64];
+  const uint32_t t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const uint32_t nb = K / kBlock, nblk_padded = (nb + 3) & ~3u, waves = blockDim.x >> 6;
+  const uint16_t* xrow = x + (int64_t)t * ldx;
+  uint4 held[kHold][4];
+#pragma unroll
+  for (int q = 0; q < kHold; ++q) {
+    const uint32_t b = tid + q * blockDim.x;
+    load_block(xrow + (int64_t)(b < nb ? b : 0) * kBlock, held[q]);
+  }
+  auto fold = [&](uint32_t q, const uint4 (&raw)[4]) {
+    double s = tid + q * blockDim.x < nb ? block_sum_sq(raw) : 0.0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s = s + __shfl_xor(s, d, 64);
+    if (lane == 0) part[q * waves + (tid >> 6)] = s;
+  };
+  uint32_t passes = 0;
+#pragma unroll
+  for (int q = 0; q < kHold; ++q) {
+    if (q * blockDim.x >= nb) break;
+    fold(q, held[q]);
+    ++passes;
+  }
+  for (; passes * blockDim.x < nb; ++passes) {
+    uint4 raw[4];
+    const uint32_t b = tid + passes * blockDim.x;
+    load_block(xrow + (int64_t)(b < nb ? b : 0) * kBlock, raw);
+    fold(passes, raw);
+  }
+  __syncthreads();
+  double root = lane < passes * waves ? part[lane] : 0.0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) root = root + __shfl_xor(root, d, 64);
+  const float r = (float)(1.0 / sqrt(root / (double)K + (double)eps));
+  if (r_out && tid == 0) r_out[t] = r;
+  auto emit = [&](uint32_t b, const uint4 (&raw)[4]) {
+    if (b >= nblk_padded) return;
+    uint4 c = make_uint4(0, 0, 0, 0);  // a block of a partial last stage
+    uint32_t e = 0;
+    if (b < nb) {
+      float xv[32];
+      widen_block(raw, xv);
+      normalize_block(xv, r);
+      if constexpr (kGamma) {
+        uint4 graw[4];
+        load_block(gamma + (int64_t)b * kBlock, graw);
+        times_gamma(xv, graw);
+      }
+      e = e8m0_from_amax_bits(amax_bits32(xv));
+      c = quantize32(xv, scale_from_e8m0(e));
+    }
+    *reinterpret_cast<uint4*>(codes + code_offset(t, b, rows)) = c;
+    scales[scale_index(t, b, rows)] = (uint8_t)e;
+  };
+#pragma unroll
+  for (int q = 0; q < kHold; ++q) emit(tid + q * blockDim.x, held[q]);
+  for (uint32_t b = tid + kHold * blockDim.x; b < nblk_padded; b += blockDim.x) {
+    uint4 raw[4];
+    load_block(xrow + (int64_t)(b < nb ? b : 0) * kBlock, raw);
+    emit(b, raw);
   }
 }
 
@@ -505,30 +574,16 @@ hipError_t launch_prepare(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, 
 
 hipError_t launch_quantize_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma, float eps,
                                float* rms_scale, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
-#define SHARQ_QUANT_ROWS(GG, QQ)                                                                                      \
-  do {                                                                                                               \
-    static int resident[64] = {};                                                                                    \
-    const uint64_t cap = resident_waves(reinterpret_cast<const void*>(&prepare_rms_rows_kernel<0, 0, GG, QQ>),      \
-                                        resident);                                                                   \
-    const uint64_t per_wave = ((uint64_t)T + cap - 1) / cap;                                                         \
-    const uint64_t waves = ((uint64_t)T + per_wave - 1) / per_wave;                                                  \
-    hipLaunchKernelGGL((prepare_rms_rows_kernel<0, 0, GG, QQ>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0,    \
-                       stream, x, ldx, gamma, (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales, nullptr,     \
-                       nullptr, nullptr);                                                                            \
-  } while (0)
-#define SHARQ_QUANT_RMS(GG)                                                                                          \
-  hipLaunchKernelGGL((prepare_rms_kernel<0, 0, GG>), dim3((unsigned)((T + kRmsRows - 1) / kRmsRows)), dim3(256), 0, \
-                     stream, x, ldx, gamma, (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales, nullptr,       \
-                     nullptr, nullptr)
-  if (K <= 2048) {
-    if (gamma) SHARQ_QUANT_ROWS(true, 1); else SHARQ_QUANT_ROWS(false, 1);
-  } else if (K <= 4096) {
-    if (gamma) SHARQ_QUANT_ROWS(true, 2); else SHARQ_QUANT_ROWS(false, 2);
+  const unsigned threads = K <= 64 * kBlock ? 64 : K <= 128 * kBlock ? 128 : 256;
+#define SHARQ_QUANT_RMS(GG, HOLD)                                                                                   \
+  hipLaunchKernelGGL((quantize_rms_kernel<GG, HOLD>), dim3((unsigned)T), dim3(threads), 0, stream, x, ldx, gamma, \
+                     (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales)
+  if (K <= 256 * kBlock) {
+    if (gamma) SHARQ_QUANT_RMS(true, 1); else SHARQ_QUANT_RMS(false, 1);
   } else {
-    if (gamma) SHARQ_QUANT_RMS(true); else SHARQ_QUANT_RMS(false);
+    if (gamma) SHARQ_QUANT_RMS(true, 2); else SHARQ_QUANT_RMS(false, 2);
   }
 #undef SHARQ_QUANT_RMS
-#undef SHARQ_QUANT_ROWS
   return hipGetLastError();
 }
 
