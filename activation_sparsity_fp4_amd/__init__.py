@@ -91,8 +91,8 @@ def _torch():
 
 
 def _stream(device) -> int:
-    torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    """The device's current stream (without making a torch.cuda.Stream of it, which takes 2 us a call)."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t) -> int:
@@ -103,7 +103,7 @@ def _need(t, dtype, name, ndim=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -112,20 +112,22 @@ def _need(t, dtype, name, ndim=None):
 
 
 def _same_device(first, *others):
+    device = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
 
 
 def _run(name, device, *args):
     """Enqueue an entry point on the device's current stream and raise on a bad status."""
     torch = _torch()
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             st = _lib.call(name, *args, _stream(device))
     else:
         st = _lib.call(name, *args, _stream(device))
-    _lib.check(name, st)
+    if st:
+        _lib.check(name, st)
 
 
 def _check_stage_major(codes, scales, R, K, name):
@@ -739,13 +741,14 @@ def unpack_stage_major(codes, scales, K: int):
 def _check_mx(t, name, ndim=3):
     """An MXFP4 tensor's codes and scales are contiguous, stage-major and fit its K."""
     torch = _torch()
-    _need(t.codes, torch.uint8, name + ".codes", ndim)
-    _need(t.scales, torch.uint8, name + ".scales", ndim)
-    lead = tuple(t.codes.shape[:-1])
-    if lead[-2] != stages(t.K) or t.codes.shape[-1] != 64 or tuple(t.scales.shape) != lead + (4,):
+    codes, scales = t.codes, t.scales
+    _need(codes, torch.uint8, name + ".codes", ndim)
+    _need(scales, torch.uint8, name + ".scales", ndim)
+    shape, sshape = codes.shape, scales.shape
+    if shape[-3] != stages(t.K) or shape[-1] != 64 or sshape[:-1] != shape[:-1] or sshape[-1] != 4:
         raise ValueError(f"{name}: expected stage-major codes [.., {stages(t.K)}, R, 64] and scales "
-                         f"[.., {stages(t.K)}, R, 4], got {tuple(t.codes.shape)} and {tuple(t.scales.shape)}")
-    if not (t.codes.is_contiguous() and t.scales.is_contiguous()):
+                         f"[.., {stages(t.K)}, R, 4], got {tuple(shape)} and {tuple(sshape)}")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous")
 
 
@@ -781,12 +784,14 @@ def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True)
     dtype, number = _out_dtype(out, dtype)
     dev = a.codes.device
     if out is None:
-        out = torch.empty((T, O), dtype=dtype, device=dev)
-    _check_matrix(out, dtype, T, O, "out")
+        out, ldy = torch.empty((T, O), dtype=dtype, device=dev), O
+    else:
+        _check_matrix(out, dtype, T, O, "out")
+        ldy = out.stride(0) if T > 1 else O
     _same_device(a.codes, a.scales, w.codes, w.scales, out)
     ws = _scratch(dev, _lib.call("sharq_linear_mxfp4_workspace_bytes", T, O, K) if split_k else 0)
     _run("sharq_linear_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-         T, O, K, out.data_ptr(), max(out.stride(0), O), number, _ptr(ws), 0 if ws is None else ws.numel())
+         T, O, K, out.data_ptr(), ldy, number, _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 
@@ -852,8 +857,9 @@ def linear_grouped_mxfp4(a: MXFP4, w: MXFP4, seg_offsets, a_rows=None, out=None,
     dtype, number = _out_dtype(out, dtype)
     if out is None:
         out = torch.empty((P, O), dtype=dtype, device=a.codes.device)
-    _check_matrix(out, dtype, P, O, "out", contiguous=True)
-    _same_device(a.codes, out)
+    else:
+        _check_matrix(out, dtype, P, O, "out", contiguous=True)
+        _same_device(a.codes, out)
     _run("sharq_linear_grouped_mxfp4", a.codes.device, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
          seg_offsets.data_ptr(), E, w.codes.data_ptr(), w.scales.data_ptr(), P, O, a.K, out.data_ptr(), number)
     return out
@@ -916,8 +922,8 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     torch = _torch()
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
-    kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if logits.dtype not in kinds:
+    kind = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     _need(logits, logits.dtype, "logits", 2)
     T, E = logits.shape
@@ -937,15 +943,14 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
             raise ValueError("num_tokens must hold one value")
     _same_device(logits, bias, num_tokens)
     dev = logits.device
-    r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
-                torch.empty((T, k), dtype=torch.float32, device=dev),
-                torch.empty(E + 1, dtype=torch.int32, device=dev),
-                torch.empty(T * k, dtype=torch.int32, device=dev),
-                torch.empty((T, k), dtype=torch.int32, device=dev))
-    ws = _scratch(dev, _lib.call("sharq_moe_route_workspace_bytes", T, E))
-    _run("sharq_moe_route", dev, logits.data_ptr(), kinds[logits.dtype], T, E,
-         logits.stride(0) if T > 1 else E, _ptr(bias), k, _SCORES[score], groups,
-         groups if top_groups is None else top_groups, _GROUP_SCORES[group_score], int(renormalize), float(scale),
-         _ptr(num_tokens), r.expert.data_ptr(), r.weight.data_ptr(), r.seg_offsets.data_ptr(), r.a_rows.data_ptr(),
-         r.pair_index.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
+    # one allocation for the four [T, k] arrays (four take longer than a small call's kernel); a_rows first, 16-byte
+    # aligned as linear_grouped asks for it
+    a_rows, expert, pair_index, weight = torch.empty((4, T, k), dtype=torch.int32, device=dev).unbind(0)
+    r = Routing(expert, weight.view(torch.float32), torch.empty(E + 1, dtype=torch.int32, device=dev),
+                a_rows.view(-1), pair_index)
+    ws = _scratch(dev, _lib.call("sharq_moe_route_workspace_bytes", T, E)) if T > 1 else None
+    _run("sharq_moe_route", dev, logits.data_ptr(), kind, T, E, logits.stride(0) if T > 1 else E, _ptr(bias), k,
+         _SCORES[score], groups, groups if top_groups is None else top_groups, _GROUP_SCORES[group_score],
+         int(renormalize), float(scale), _ptr(num_tokens), expert.data_ptr(), weight.data_ptr(),
+         r.seg_offsets.data_ptr(), a_rows.data_ptr(), pair_index.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return r

@@ -2,15 +2,18 @@
 // each token, their weights, and the dispatch plan that the grouped GEMMs and
 // the combine read (pairs sorted by expert, tokens in order inside one).
 //
-// Selection orders the experts by a key: the logit itself without a bias (the
+// Selection orders the experts by a value: the logit itself without a bias (the
 // scores are monotone in it), score + bias in float64 with one (float32 scores
-// would tie or swap experts that the definition tells apart). Keys become
-// unsigned integers of the same order, 0 for an expert that cannot be chosen.
-// A token's experts lie in LANES lanes, NE neighbouring ones in each, so of
-// equal keys the lowest lane and the lowest register hold the lowest expert. A
-// round takes the largest key: a register maximum, a rotation maximum over the
-// 16-lane row (four lane-crossing maxima, no LDS), a ballot for the first lane
-// that has it. Four tokens share a wave for up to 256 experts.
+// would tie or swap experts that the definition tells apart). A key is the
+// value rounded to float32 as an unsigned integer of the same order, 0 for an
+// expert that cannot be chosen; rounding is monotone, so only experts of equal
+// keys need their float64 values compared, and that is rare. A token's experts
+// lie in LANES lanes, NE neighbouring ones in each, so of equal values the
+// lowest lane and the lowest register hold the lowest expert. A round takes the
+// largest key: a register maximum, a rotation maximum over the 16-lane row
+// (four lane-crossing maxima, no LDS), a ballot for the first lane that has it.
+// Four tokens share a wave for up to 256 experts, and tokens of different
+// waves do not wait for each other.
 //
 // Plan: workgroup c owns a chunk of consecutive tokens (at most 256 chunks)
 // and counts its pairs per expert. The second kernel adds up the counts of all
@@ -71,10 +74,21 @@ __device__ __forceinline__ uint64_t ordered(double x) {
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-__device__ __forceinline__ float load_logit(const void* x, int dtype, int64_t i) {
-  if (dtype == 0) return static_cast<const float*>(x)[i];
-  if (dtype == 1) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
-  return (float)static_cast<const _Float16*>(x)[i];
+// NE logits of a row from expert e0 on; -inf for what cannot be chosen (no such
+// expert, a padding row, -inf or NaN), +inf as the largest finite value.
+template <int NE, class T>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int e0, int E, bool live, float (&x)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    float v = -__builtin_huge_valf();
+    if (live && e0 + i < E) {
+      if constexpr (std::is_same<T, uint16_t>::value)
+        v = __uint_as_float((uint32_t)row[e0 + i] << 16);
+      else
+        v = (float)row[e0 + i];
+    }
+    x[i] = v > -__builtin_huge_valf() ? fminf(v, 3.4028234663852886e38f) : -__builtin_huge_valf();
+  }
 }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
@@ -117,17 +131,19 @@ __device__ void plan_chunk(const RouteArgs& a, int64_t t0, int64_t t1, int* tota
   // entries behind the last pair
   for (int64_t p = carry + (int64_t)chunk * nthreads + tid; p < a.T * a.k; p += (int64_t)chunks * nthreads)
     a.a_rows[p] = -1;
+  const float per_token = 1.0f / (float)a.k;
+  auto token_of = [&](int p) { return (int)(((float)p + 0.5f) * per_token); };  // p / k, exact for p < 4096
   for (int64_t s0 = t0; s0 < t1; s0 += 64) {
     const int pairs = (int)((t1 - s0 < 64 ? t1 - s0 : 64) * a.k);
     for (int e = tid; e < a.E; e += nthreads) bits[e] = 0;
     __syncthreads();
     for (int p = tid; p < pairs; p += nthreads) {
       const int e = a.expert[s0 * a.k + p];
-      if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&bits[e]), 1ull << (p / a.k));
+      if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&bits[e]), 1ull << token_of(p));
     }
     __syncthreads();
     for (int p = tid; p < pairs; p += nthreads) {
-      const int e = a.expert[s0 * a.k + p], t = p / a.k;
+      const int e = a.expert[s0 * a.k + p], t = token_of(p);
       int at = -1;
       if (e >= 0) {
         at = before[e] + __popcll(bits[e] & ((1ull << t) - 1));
@@ -141,24 +157,87 @@ __device__ void plan_chunk(const RouteArgs& a, int64_t t0, int64_t t1, int* tota
   }
 }
 
-// Routes the tokens of chunk blockIdx.x. LDS: E counts, then (one chunk) the
-// plan's arrays, then k slots (expert, logit) of every token in flight, then,
-// with groups, a double per expert and per group of every token in flight.
+// LDS written by a wave and read by the same wave: in order as it is, kept so by the compiler.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Doubles of LDS that the groups of a token take: its values (or the two
+// largest of each lane) and the groups' scores.
+__host__ __device__ constexpr int group_doubles(int E, int groups, int lanes) {
+  return (E > 2 * lanes ? E : 2 * lanes) + groups;
+}
+
+__device__ __forceinline__ void take_two(double v, double& first, double& second) {
+  second = fmax(second, fmin(first, v));
+  first = fmax(first, v);
+}
+
+// Clears the keys of experts outside the token's top_groups groups. v: what
+// the groups compare, -inf for an expert that cannot be chosen; buf: the
+// token's group_doubles in LDS.
+template <int LANES, int NE>
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, const double (&v)[NE], uint32_t (&key)[NE], int lt,
+                                            double* buf) {
+  const int size = a.E / a.groups;
+  double* gscore = buf + group_doubles(a.E, 0, LANES);
+  const bool whole = size % NE == 0;  // a lane's experts belong to one group
+  if (whole) {
+    double first = kNegInf, second = kNegInf;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) take_two(v[i], first, second);
+    buf[2 * lt] = first;
+    buf[2 * lt + 1] = second;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lt * NE + i < a.E) buf[lt * NE + i] = v[i];
+  }
+  wave_sync();
+  const int per = whole ? 2 * (size / NE) : size;  // entries of a group
+  for (int g = lt; g < a.groups; g += LANES) {
+    double first = kNegInf, second = kNegInf;
+    for (int e = g * per; e < (g + 1) * per; ++e) take_two(buf[e], first, second);
+    gscore[g] = first + (a.sum2 && second > kNegInf ? second : 0.0);
+  }
+  wave_sync();
+  int g = lt * NE / size, in = lt * NE - g * size, seen = -1;
+  bool keep = false;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    if (g != seen && g < a.groups) {
+      const double mine = gscore[g];
+      int rank = 0;
+      for (int o = 0; o < a.groups; ++o) {
+        const double other = gscore[o];
+        rank += other > mine || (other == mine && o < g);
+      }
+      keep = rank < a.top_groups;
+      seen = g;
+    }
+    if (!keep) key[i] = 0;
+    if (++in == size) in = 0, ++g;
+  }
+}
+
+// Routes the tokens of chunk blockIdx.x. LDS: bit masks, counts and places of
+// the experts, then k slots (expert, logit) of every token in flight, then,
+// with groups, group_doubles of every token in flight.
 template <int LANES, int NE, bool kBias>
-__global__ __launch_bounds__(1024) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
-  using Key = typename std::conditional<kBias, uint64_t, uint32_t>::type;
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int lt = lane % LANES;                     // lane of the token
-  const int slot = tid / LANES;                    // token of the workgroup in flight
+  const int lt = lane % LANES;      // lane of the token
+  const int slot = tid / LANES;     // token of the workgroup in flight
   const int flight = blockDim.x / LANES;
   uint64_t* bits = reinterpret_cast<uint64_t*>(lds);
   int* counts = reinterpret_cast<int*>(bits + a.E);
   int* before = counts + a.E;
   int2* chosen = reinterpret_cast<int2*>(before + a.E) + (int64_t)slot * a.k;
-  double* gval = reinterpret_cast<double*>(reinterpret_cast<int2*>(before + a.E) + (int64_t)flight * a.k) +
-                 (int64_t)slot * (a.E + a.groups);
-  double* gscore = gval + a.E;
+  double* gbuf = reinterpret_cast<double*>(reinterpret_cast<int2*>(before + a.E) + (int64_t)flight * a.k) +
+                 (int64_t)slot * group_doubles(a.E, a.groups, LANES);
   for (int e = tid; e < a.E; e += blockDim.x) counts[e] = 0, before[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * chunk_tokens;
@@ -166,100 +245,95 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(RouteArgs a, int64_t ch
   const int64_t live_rows = a.num_tokens ? (int64_t)*a.num_tokens : a.T;
   const bool softmax = a.sigmoid == 0;
   auto add = [](double p, double q) { return p + q; };
-  for (int64_t tb = t0; tb < t1; tb += flight) {
-    const int64_t t = tb + slot;
+  for (int64_t t = t0 + slot; t - lane / LANES < t1; t += flight) {  // uniform over a wave
     const bool row = t < t1 && t < live_rows;
-    // logits; an expert that cannot be chosen has -inf
     float x[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = lt * NE + i;
-      const float v = row && e < a.E ? load_logit(a.logits, a.dtype, t * a.ld + e) : kNegInf;
-      x[i] = v > kNegInf ? fminf(v, 3.4028234663852886e38f) : kNegInf;  // NaN: -inf
-    }
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < NE; ++i) top = fmaxf(top, x[i]);
-    top = token_reduce<LANES>(top, [](float p, float q) { return fmaxf(p, q); });
-    const double ref = top > kNegInf ? (double)top : 0.0;
-    double total = 1.0;
+    const int64_t at_row = row ? t * a.ld : 0;
+    if (a.dtype == 0) load_row<NE>(static_cast<const float*>(a.logits) + at_row, lt * NE, a.E, row, x);
+    else if (a.dtype == 1) load_row<NE>(static_cast<const uint16_t*>(a.logits) + at_row, lt * NE, a.E, row, x);
+    else load_row<NE>(static_cast<const _Float16*>(a.logits) + at_row, lt * NE, a.E, row, x);
+    double ref = 0.0, total = 1.0;  // softmax: the row's largest logit, and the sum of exp(x - ref)
     const bool all_scores = kBias || (a.groups > 1 && a.sum2);
     if (softmax && (all_scores || !a.renormalize)) {
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < NE; ++i) top = fmaxf(top, x[i]);
+      top = token_reduce<LANES>(top, [](float p, float q) { return fmaxf(p, q); });
+      if (top > kNegInf) ref = (double)top;
       total = 0.0;
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (x[i] > kNegInf) total += exp((double)x[i] - ref);
+      for (int i = 0; i < NE; ++i) total += exp((double)x[i] - ref);  // 0 for -inf
       total = token_reduce<LANES>(total, add);
     }
-    Key key[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const bool live = x[i] > kNegInf;
-      const int e = lt * NE + i;
-      double v = kNegInf;  // what the groups compare
-      if constexpr (kBias) {
-        if (live) {
-          v = (softmax ? exp((double)x[i] - ref) / total : sigmoid64(x[i])) + (double)a.bias[e];
-          if (!(v > kNegInf)) v = kNegInf;
-        }
-        key[i] = v > kNegInf ? ordered(v) : 0;
-      } else {
-        key[i] = live ? ordered(x[i]) : 0;
-        if (a.groups > 1 && live)
-          v = !a.sum2 ? (double)x[i] : softmax ? exp((double)x[i] - ref) / total : sigmoid64(x[i]);
-      }
-      if (a.groups > 1 && e < a.E) gval[e] = v;
-    }
-    if (a.groups > 1) {
-      __syncthreads();
-      const int size = a.E / a.groups;
-      for (int g = lt; g < a.groups; g += LANES) {
-        double first = kNegInf, second = kNegInf;
-        for (int e = g * size; e < (g + 1) * size; ++e) {
-          const double v = gval[e];
-          second = fmax(second, fmin(first, v));
-          first = fmax(first, v);
-        }
-        gscore[g] = first + (a.sum2 && second > kNegInf ? second : 0.0);
-      }
-      __syncthreads();
-      int g = lt * NE / size, in = lt * NE - g * size, seen = -1;
-      bool keep = false;
+    uint32_t key[NE];
+    double value[kBias ? NE : 1];
+    if constexpr (kBias) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        if (g != seen && g < a.groups) {
-          const double mine = gscore[g];
-          int rank = 0;
-          for (int o = 0; o < a.groups; ++o) rank += gscore[o] > mine || (gscore[o] == mine && o < g);
-          keep = rank < a.top_groups;
-          seen = g;
-        }
-        if (!keep) key[i] = 0;
-        if (++in == size) in = 0, ++g;
+        const int e = min(lt * NE + i, a.E - 1);
+        double v = (softmax ? exp((double)x[i] - ref) / total : sigmoid64(x[i])) + (double)a.bias[e];
+        v = x[i] > kNegInf && v > kNegInf ? v : (double)kNegInf;
+        value[i] = v;
+        key[i] = v > kNegInf ? ordered((float)v) : 0;
+      }
+      if (a.groups > 1) keep_groups<LANES, NE>(a, value, key, lt, gbuf);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) key[i] = x[i] > kNegInf ? ordered(x[i]) : 0;
+      if (a.groups > 1) {
+        double v[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          v[i] = !(x[i] > kNegInf) ? (double)kNegInf
+                 : !a.sum2         ? (double)x[i]
+                 : softmax         ? exp((double)x[i] - ref) / total
+                                   : sigmoid64(x[i]);
+        keep_groups<LANES, NE>(a, v, key, lt, gbuf);
       }
     }
     // k rounds
     for (int j = 0; j < a.k; ++j) {
-      Key head = key[0];
+      uint32_t head = key[0];
 #pragma unroll
-      for (int i = 1; i < NE; ++i) head = key[i] > head ? key[i] : head;
-      const Key best = token_reduce<LANES>(head, [](Key p, Key q) { return p > q ? p : q; });
-      const uint64_t have = __ballot(head == best && best != 0);
-      const uint64_t mine = LANES == 64 ? have : (have >> (lane & ~(LANES - 1))) & ((1ull << (LANES & 63)) - 1);
-      const bool winner = mine != 0 && lt == __ffsll((unsigned long long)mine) - 1;
-      int at = -1;
+      for (int i = 1; i < NE; ++i) head = max(head, key[i]);
+      const uint32_t best = token_reduce<LANES>(head, [](uint32_t p, uint32_t q) { return max(p, q); });
+      int at = 0, same = 0;
 #pragma unroll
-      for (int i = NE - 1; i >= 0; --i)
-        if (winner && key[i] == best) at = i;
+      for (int i = NE - 1; i >= 0; --i) {
+        at = key[i] == best ? i : at;
+        if constexpr (kBias) same += key[i] == best;
+      }
+      bool mine = head == best && best != 0;
+      uint64_t have = __ballot(mine);
+      auto of_token = [&](uint64_t m) {
+        return LANES == 64 ? m : (m >> (lane & ~(LANES - 1))) & ((1ull << (LANES & 63)) - 1);
+      };
+      if constexpr (kBias) {  // several experts of this key: by their float64 values
+        const uint64_t have_token = of_token(have);
+        if (__any((mine && same > 1) || (have_token & (have_token - 1)) != 0)) {
+          uint64_t top = 0;
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (at == i) {
-          chosen[j] = make_int2(lt * NE + i, (int)__float_as_uint(x[i]));
-          key[i] = 0;
+          for (int i = 0; i < NE; ++i) top = key[i] == best && best != 0 ? max(top, ordered(value[i])) : top;
+          const uint64_t highest = token_reduce<LANES>(top, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
+          mine = mine && top == highest;
+          have = __ballot(mine);
+#pragma unroll
+          for (int i = NE - 1; i >= 0; --i) at = key[i] == best && ordered(value[i]) == highest ? i : at;
         }
-      if (mine == 0 && lt == 0) chosen[j] = make_int2(-1, 0);
+      }
+      const uint64_t token = of_token(have);
+      const bool winner = mine && (token & ((1ull << lt) - 1)) == 0;
+      if (winner || (token == 0 && lt == 0)) {
+        float logit = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) logit = at == i ? x[i] : logit;
+        chosen[j] = make_int2(winner ? lt * NE + at : -1, (int)__float_as_uint(logit));
+      }
+      if (!winner) at = -1;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) key[i] = at == i ? 0 : key[i];
     }
-    __syncthreads();
+    wave_sync();
     // weights, k slots over the token's lanes; renormalised ones relative to the largest chosen score, so that
     // they do not depend on how small the scores are
     double v[kSlots / LANES], w[kSlots / LANES], high = kNegInf, sum = 0.0;
@@ -296,8 +370,9 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(RouteArgs a, int64_t ch
         if (e >= 0) atomicAdd(&counts[e], 1);
       }
     }
-    __syncthreads();
+    wave_sync();
   }
+  __syncthreads();
   if (chunks == 1) {
     __threadfence_block();
     plan_chunk(a, t0, t1, counts, before, bits, 0, 1);
@@ -345,11 +420,11 @@ int64_t chunk_tokens(int64_t T) {
 
 template <int LANES, int NE>
 void launch_route(const RouteArgs& a, int64_t per, int chunks, hipStream_t stream) {
-  // tokens in flight: the chunk's, at most 1024 threads' worth and 64 KB of LDS
-  const int64_t token_bytes = 8 * a.k + (a.groups > 1 ? 8 * (a.E + a.groups) : 0);
+  // tokens in flight: the chunk's, at most 256 threads' worth and 64 KB of LDS
+  const int64_t token_bytes = 8 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups, LANES) : 0);
   const int64_t fixed = 16 * (int64_t)a.E;
   int64_t flight = (a.T < per ? a.T : per);
-  if (flight > 1024 / LANES) flight = 1024 / LANES;
+  if (flight > 256 / LANES) flight = 256 / LANES;
   if (flight < 1) flight = 1;
   while (flight > 1 && fixed + flight * token_bytes > 64 * 1024) flight /= 2;
   int threads = (int)((flight * LANES + 63) / 64 * 64);
