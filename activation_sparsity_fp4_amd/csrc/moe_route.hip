@@ -3,17 +3,18 @@
 // the combine read (pairs sorted by expert, tokens in order inside one).
 //
 // Selection orders the experts by a value: the logit itself without a bias (the
-// scores are monotone in it), score + bias in float64 with one (float32 scores
-// would tie or swap experts that the definition tells apart). A key is the
-// value rounded to float32 as an unsigned integer of the same order, 0 for an
-// expert that cannot be chosen; rounding is monotone, so only experts of equal
-// keys need their float64 values compared, and that is rare. A token's experts
-// lie in LANES lanes, NE neighbouring ones in each, so of equal values the
-// lowest lane and the lowest register hold the lowest expert. A round takes the
-// largest key: a register maximum, a rotation maximum over the 16-lane row
-// (four lane-crossing maxima, no LDS), a ballot for the first lane that has it.
-// Four tokens share a wave for up to 256 experts, and tokens of different
-// waves do not wait for each other.
+// scores are monotone in it), score + bias in float64 with one. Scores are
+// first taken in float32 with a bound on their error; only where two of the
+// values that decide (a round's largest and the next, two groups) lie within
+// the bound is the wave's selection done again in float64, so the choice is
+// float64's at about a third of its time (16384 x 256 with groups: 50 us with
+// every score in float64). A token's experts lie in LANES lanes, NE
+// neighbouring ones in each, so of equal values the lowest lane and the lowest
+// register hold the lowest expert. A round takes the largest value as an
+// unsigned integer of the same order (0: cannot be chosen): a register
+// maximum, a rotation maximum over the 16-lane row and lane swaps beyond (no
+// LDS), a ballot for the first lane that has it. Four tokens share a wave for
+// up to 128 experts, and tokens of different waves do not wait for each other.
 //
 // Plan: workgroup c owns a chunk of consecutive tokens (at most 256 chunks)
 // and counts its pairs per expert. The second kernel adds up the counts of all
@@ -51,17 +52,34 @@ __device__ __forceinline__ float row_ror(float v) {
   return __uint_as_float(row_ror<CTRL>(__float_as_uint(v)));
 }
 
-// Reduction over a token's LANES lanes (16 or 64), the result in all of them.
+// f of a lane's value and that of the lane 16 or 32 away (rows of 16 or halves swapped, no LDS).
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+template <int D>
+__device__ __forceinline__ v2u lane_swap(uint32_t v) {
+  if constexpr (D == 16) return __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  else return __builtin_amdgcn_permlane32_swap(v, v, false, false);
+}
+template <int D, class T, class F>
+__device__ __forceinline__ T swap_reduce(T v, F f) {
+  if constexpr (sizeof(T) == 4) {
+    const v2u p = lane_swap<D>(__builtin_bit_cast(uint32_t, v));
+    return f(__builtin_bit_cast(T, (uint32_t)p[0]), __builtin_bit_cast(T, (uint32_t)p[1]));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const v2u lo = lane_swap<D>((uint32_t)u), hi = lane_swap<D>((uint32_t)(u >> 32));
+    return f(__builtin_bit_cast(T, (uint64_t)hi[0] << 32 | lo[0]), __builtin_bit_cast(T, (uint64_t)hi[1] << 32 | lo[1]));
+  }
+}
+
+// Reduction over a token's LANES lanes (16, 32 or 64), the result in all of them.
 template <int LANES, class T, class F>
 __device__ __forceinline__ T token_reduce(T v, F f) {
   v = f(v, row_ror<0x128>(v));
   v = f(v, row_ror<0x124>(v));
   v = f(v, row_ror<0x122>(v));
   v = f(v, row_ror<0x121>(v));
-  if constexpr (LANES == 64) {
-    v = f(v, __shfl_xor(v, 16, 64));
-    v = f(v, __shfl_xor(v, 32, 64));
-  }
+  if constexpr (LANES >= 32) v = swap_reduce<16>(v, f);
+  if constexpr (LANES >= 64) v = swap_reduce<32>(v, f);
   return v;
 }
 
@@ -72,6 +90,12 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ uint64_t ordered(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
   return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+__device__ __forceinline__ float load_logit(const void* x, int dtype, int64_t i) {
+  if (dtype == 0) return static_cast<const float*>(x)[i];
+  if (dtype == 1) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
+  return (float)static_cast<const _Float16*>(x)[i];
 }
 
 // NE logits of a row from expert e0 on; -inf for what cannot be chosen (no such
@@ -170,24 +194,27 @@ __host__ __device__ constexpr int group_doubles(int E, int groups, int lanes) {
   return (E > 2 * lanes ? E : 2 * lanes) + groups;
 }
 
-__device__ __forceinline__ void take_two(double v, double& first, double& second) {
-  second = fmax(second, fmin(first, v));
-  first = fmax(first, v);
+template <class V>
+__device__ __forceinline__ void take_two(V v, V& first, V& second) {
+  second = max(second, min(first, v));
+  first = max(first, v);
 }
 
 // Clears the keys of experts outside the token's top_groups groups. v: what
 // the groups compare, -inf for an expert that cannot be chosen; buf: the
-// token's group_doubles in LDS.
-template <int LANES, int NE>
-__device__ __forceinline__ void keep_groups(const RouteArgs& a, const double (&v)[NE], uint32_t (&key)[NE], int lt,
-                                            double* buf) {
+// token's group_doubles in LDS. True where two groups' scores are at most
+// `near` apart (never for near < 0).
+template <int LANES, int NE, class V, class Key>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& a, const V (&v)[NE], Key (&key)[NE], int lt, double* lds,
+                                            V near) {
   const int size = a.E / a.groups;
-  double* gscore = buf + group_doubles(a.E, 0, LANES);
+  V* buf = reinterpret_cast<V*>(lds);
+  V* gscore = buf + group_doubles(a.E, 0, LANES);
   const bool whole = size % NE == 0;  // a lane's experts belong to one group
   if (whole) {
-    double first = kNegInf, second = kNegInf;
+    V first = kNegInf, second = kNegInf;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) take_two(v[i], first, second);
+    for (int i = 0; i < NE; ++i) take_two<V>(v[i], first, second);
     buf[2 * lt] = first;
     buf[2 * lt + 1] = second;
   } else {
@@ -198,21 +225,22 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const double (&v
   wave_sync();
   const int per = whole ? 2 * (size / NE) : size;  // entries of a group
   for (int g = lt; g < a.groups; g += LANES) {
-    double first = kNegInf, second = kNegInf;
-    for (int e = g * per; e < (g + 1) * per; ++e) take_two(buf[e], first, second);
-    gscore[g] = first + (a.sum2 && second > kNegInf ? second : 0.0);
+    V first = kNegInf, second = kNegInf;
+    for (int e = g * per; e < (g + 1) * per; ++e) take_two<V>(buf[e], first, second);
+    gscore[g] = first + (a.sum2 && second > (V)kNegInf ? second : (V)0);
   }
   wave_sync();
   int g = lt * NE / size, in = lt * NE - g * size, seen = -1;
-  bool keep = false;
+  bool keep = false, close = false;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     if (g != seen && g < a.groups) {
-      const double mine = gscore[g];
+      const V mine = gscore[g];
       int rank = 0;
       for (int o = 0; o < a.groups; ++o) {
-        const double other = gscore[o];
+        const V other = gscore[o];
         rank += other > mine || (other == mine && o < g);
+        close |= o != g && fabs(other - mine) <= near;
       }
       keep = rank < a.top_groups;
       seen = g;
@@ -220,13 +248,127 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const double (&v
     if (!keep) key[i] = 0;
     if (++in == size) in = 0, ++g;
   }
+  wave_sync();
+  return close;
+}
+
+__device__ __forceinline__ double score_exp(double x) { return exp(x); }
+__device__ __forceinline__ float score_exp(float x) { return __expf(x); }
+__device__ __forceinline__ double score_inverse(double x) { return 1.0 / x; }
+__device__ __forceinline__ float score_inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The k best experts of a wave's tokens, x their logits (-inf: cannot be
+// chosen), into chosen[j] (an expert or -1). True where values of type V
+// did not tell (a uniform answer; V = double always does).
+//
+// Error of the float32 scores, u = 2^-24: exp(y), y a rounded difference, is
+// off by at most (2.5 |y| + 2) u of it (the argument's two roundings, log2(e)'s
+// and the instruction's), the reciprocal by 2 u, an addition by u. A sigmoid
+// s = 1 / (1 + e): s (1 - s) (2.5 |x| + 2) u + 3 s u < 4e-7. A softmax score p =
+// e / sum of at most 21 rounded additions of terms off by a mean of at most
+// (2.5 ln 1024 + 2) u: p (2.5 |y| + 2 + 21 + 20 + 3) u < 3.5e-6 / sum, as p <=
+// 1 / sum and p |y| < 0.37 / sum. Adding the bias rounds by u of the result.
+// Two values closer than twice the bound are taken for close.
+template <int LANES, int NE, bool kBias, class V>
+__device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE], int lane, int* chosen,
+                                       double* gbuf) {
+  using Key = typename std::conditional<sizeof(V) == 8, uint64_t, uint32_t>::type;
+  constexpr bool kRough = kBias && sizeof(V) == 4;
+  const int lt = lane % LANES;
+  const bool softmax = a.sigmoid == 0;
+  Key key[NE];
+  V value[NE];
+  V bound = 0;
+  bool close = false;
+  const bool scores = kBias || (a.groups > 1 && a.sum2);
+  if (scores) {
+    V ref = 0, inv = 1;
+    if (softmax) {
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < NE; ++i) top = fmaxf(top, x[i]);
+      top = token_reduce<LANES>(top, [](float p, float q) { return fmaxf(p, q); });
+      if (top > kNegInf) ref = (V)top;
+      V total = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) total += score_exp((V)x[i] - ref);  // 0 for -inf
+      total = token_reduce<LANES>(total, [](V p, V q) { return p + q; });
+      inv = score_inverse(total);
+    }
+    bound = softmax ? (V)3.5e-6 * inv : (V)4e-7;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      V v = softmax ? score_exp((V)x[i] - ref) * inv : score_inverse((V)1 + score_exp(-(V)x[i]));
+      if constexpr (kBias) v += (V)a.bias[min(lt * NE + i, a.E - 1)];
+      value[i] = x[i] > kNegInf && v > (V)kNegInf ? v : (V)kNegInf;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) value[i] = (V)x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const V v = kBias ? value[i] : (V)x[i];
+    key[i] = v > (V)kNegInf ? ordered(v) : 0;
+  }
+  if (a.groups > 1) {
+    V near = -1;
+    if (sizeof(V) == 4 && scores) {  // sums of up to two values, and their rounding
+      V most = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) most = value[i] > (V)kNegInf ? max(most, (V)fabs(value[i])) : most;
+      most = token_reduce<LANES>(most, [](V p, V q) { return p > q ? p : q; });
+      near = 4 * bound + most * (V)5e-7;
+    }
+    close = keep_groups<LANES, NE, V, Key>(a, value, key, lt, gbuf, near);
+  }
+  for (int j = lt; j < a.k; j += LANES) chosen[j] = -1;
+  wave_sync();
+  // this lane's token in a ballot: the lanes below it, and all of them
+  const uint32_t shift = lane & 31 & ~(LANES - 1);
+  const uint32_t below = ((1u << (lt & 31)) - 1u) << shift;
+  const uint32_t whole = (LANES >= 32 ? 0xFFFFFFFFu : (1u << (LANES & 31)) - 1u) << shift;
+  auto lanes_of = [&](uint64_t m) { return lane < 32 ? (uint32_t)m : (uint32_t)(m >> 32); };
+  for (int j = 0; j < a.k; ++j) {
+    Key head = key[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) head = max(head, key[i]);
+    const Key best = token_reduce<LANES>(head, [](Key p, Key q) { return max(p, q); });
+    const bool has = head == best && best != 0;
+    const uint64_t have = __ballot(has);
+    if constexpr (kRough) {  // keys from `low` on are too near the best to tell
+      const float v = __uint_as_float((uint32_t)(best >> 31 ? best ^ 0x80000000u : ~best));
+      const Key low = best ? ordered(v - 2.0f * ((float)bound + fabsf(v) * 1.2e-7f)) : 1;
+      int same = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) same += key[i] >= low;
+      const uint64_t near = __ballot(same > 0);
+      const int lanes = LANES == 64 ? __popcll(near) : __popc(lanes_of(near) & whole);
+      close |= best != 0 && (same > 1 || lanes > 1);
+    }
+    const bool first = LANES == 64 ? (have & ((1ull << lt) - 1)) == 0 : (lanes_of(have) & below) == 0;
+    int at = -1;
+#pragma unroll
+    for (int i = NE - 1; i >= 0; --i) at = key[i] == best ? i : at;
+    if (!(has && first)) at = -1;
+    if (at >= 0) chosen[j] = lt * NE + at;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = at == i ? 0 : key[i];
+  }
+  wave_sync();
+  return __any(close);
 }
 
 // Routes the tokens of chunk blockIdx.x. LDS: bit masks, counts and places of
-// the experts, then k slots (expert, logit) of every token in flight, then,
+// the experts, then k slots of every token in flight, then,
 // with groups, group_doubles of every token in flight.
+// Threads of a routing workgroup: 1024 (128 registers a lane), 512 where a lane
+// holds 16 experts.
+template <int NE>
+constexpr int kRouteThreads = NE <= 8 ? 1024 : 512;
+
 template <int LANES, int NE, bool kBias>
-__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
+__global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int lt = lane % LANES;      // lane of the token
@@ -235,8 +377,8 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chu
   uint64_t* bits = reinterpret_cast<uint64_t*>(lds);
   int* counts = reinterpret_cast<int*>(bits + a.E);
   int* before = counts + a.E;
-  int2* chosen = reinterpret_cast<int2*>(before + a.E) + (int64_t)slot * a.k;
-  double* gbuf = reinterpret_cast<double*>(reinterpret_cast<int2*>(before + a.E) + (int64_t)flight * a.k) +
+  int* chosen = before + a.E + (int64_t)slot * a.k;
+  double* gbuf = reinterpret_cast<double*>(before + a.E + ((int64_t)flight * a.k + 1) / 2 * 2) +
                  (int64_t)slot * group_doubles(a.E, a.groups, LANES);
   for (int e = tid; e < a.E; e += blockDim.x) counts[e] = 0, before[e] = 0;
   __syncthreads();
@@ -252,9 +394,10 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chu
     if (a.dtype == 0) load_row<NE>(static_cast<const float*>(a.logits) + at_row, lt * NE, a.E, row, x);
     else if (a.dtype == 1) load_row<NE>(static_cast<const uint16_t*>(a.logits) + at_row, lt * NE, a.E, row, x);
     else load_row<NE>(static_cast<const _Float16*>(a.logits) + at_row, lt * NE, a.E, row, x);
+    if (select<LANES, NE, kBias, float>(a, x, lane, chosen, gbuf))
+      select<LANES, NE, kBias, double>(a, x, lane, chosen, gbuf);
     double ref = 0.0, total = 1.0;  // softmax: the row's largest logit, and the sum of exp(x - ref)
-    const bool all_scores = kBias || (a.groups > 1 && a.sum2);
-    if (softmax && (all_scores || !a.renormalize)) {
+    if (softmax && !a.renormalize) {
       float top = x[0];
 #pragma unroll
       for (int i = 1; i < NE; ++i) top = fmaxf(top, x[i]);
@@ -265,82 +408,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chu
       for (int i = 0; i < NE; ++i) total += exp((double)x[i] - ref);  // 0 for -inf
       total = token_reduce<LANES>(total, add);
     }
-    uint32_t key[NE];
-    double value[kBias ? NE : 1];
-    if constexpr (kBias) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int e = min(lt * NE + i, a.E - 1);
-        double v = (softmax ? exp((double)x[i] - ref) / total : sigmoid64(x[i])) + (double)a.bias[e];
-        v = x[i] > kNegInf && v > kNegInf ? v : (double)kNegInf;
-        value[i] = v;
-        key[i] = v > kNegInf ? ordered((float)v) : 0;
-      }
-      if (a.groups > 1) keep_groups<LANES, NE>(a, value, key, lt, gbuf);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) key[i] = x[i] > kNegInf ? ordered(x[i]) : 0;
-      if (a.groups > 1) {
-        double v[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-          v[i] = !(x[i] > kNegInf) ? (double)kNegInf
-                 : !a.sum2         ? (double)x[i]
-                 : softmax         ? exp((double)x[i] - ref) / total
-                                   : sigmoid64(x[i]);
-        keep_groups<LANES, NE>(a, v, key, lt, gbuf);
-      }
-    }
-    // k rounds
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t head = key[0];
-#pragma unroll
-      for (int i = 1; i < NE; ++i) head = max(head, key[i]);
-      const uint32_t best = token_reduce<LANES>(head, [](uint32_t p, uint32_t q) { return max(p, q); });
-      int at = 0, same = 0;
-#pragma unroll
-      for (int i = NE - 1; i >= 0; --i) {
-        at = key[i] == best ? i : at;
-        if constexpr (kBias) same += key[i] == best;
-      }
-      bool mine = head == best && best != 0;
-      uint64_t have = __ballot(mine);
-      auto of_token = [&](uint64_t m) {
-        return LANES == 64 ? m : (m >> (lane & ~(LANES - 1))) & ((1ull << (LANES & 63)) - 1);
-      };
-      if constexpr (kBias) {  // several experts of this key: by their float64 values
-        const uint64_t have_token = of_token(have);
-        if (__any((mine && same > 1) || (have_token & (have_token - 1)) != 0)) {
-          uint64_t top = 0;
-#pragma unroll
-          for (int i = 0; i < NE; ++i) top = key[i] == best && best != 0 ? max(top, ordered(value[i])) : top;
-          const uint64_t highest = token_reduce<LANES>(top, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-          mine = mine && top == highest;
-          have = __ballot(mine);
-#pragma unroll
-          for (int i = NE - 1; i >= 0; --i) at = key[i] == best && ordered(value[i]) == highest ? i : at;
-        }
-      }
-      const uint64_t token = of_token(have);
-      const bool winner = mine && (token & ((1ull << lt) - 1)) == 0;
-      if (winner || (token == 0 && lt == 0)) {
-        float logit = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) logit = at == i ? x[i] : logit;
-        chosen[j] = make_int2(winner ? lt * NE + at : -1, (int)__float_as_uint(logit));
-      }
-      if (!winner) at = -1;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) key[i] = at == i ? 0 : key[i];
-    }
-    wave_sync();
     // weights, k slots over the token's lanes; renormalised ones relative to the largest chosen score, so that
     // they do not depend on how small the scores are
     double v[kSlots / LANES], w[kSlots / LANES], high = kNegInf, sum = 0.0;
 #pragma unroll
     for (int s = 0; s < kSlots / LANES; ++s) {
       const int j = s * LANES + lt;
-      v[s] = j < a.k && chosen[j].x >= 0 ? (double)__uint_as_float((uint32_t)chosen[j].y) : kNegInf;
+      const int e = j < a.k ? chosen[j] : -1;
+      v[s] = e >= 0 ? (double)fminf(load_logit(a.logits, a.dtype, t * a.ld + e), 3.4028234663852886e38f) : kNegInf;
       high = fmax(high, v[s]);
     }
     if (a.renormalize) high = token_reduce<LANES>(high, [](double p, double q) { return fmax(p, q); });
@@ -364,7 +439,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int64_t chu
     for (int s = 0; s < kSlots / LANES; ++s) {
       const int j = s * LANES + lt;
       if (j < a.k && t < t1) {
-        const int e = chosen[j].x;
+        const int e = chosen[j];
         a.expert[t * a.k + j] = e;
         a.weight[t * a.k + j] = (float)(a.scale * (w[s] / sum));
         if (e >= 0) atomicAdd(&counts[e], 1);
@@ -420,11 +495,11 @@ int64_t chunk_tokens(int64_t T) {
 
 template <int LANES, int NE>
 void launch_route(const RouteArgs& a, int64_t per, int chunks, hipStream_t stream) {
-  // tokens in flight: the chunk's, at most 256 threads' worth and 64 KB of LDS
-  const int64_t token_bytes = 8 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups, LANES) : 0);
-  const int64_t fixed = 16 * (int64_t)a.E;
+  // tokens in flight: the chunk's, at most a workgroup's worth and 64 KB of LDS
+  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups, LANES) : 0);
+  const int64_t fixed = 16 * (int64_t)a.E + 8;  // 8: the groups' doubles are aligned
   int64_t flight = (a.T < per ? a.T : per);
-  if (flight > 256 / LANES) flight = 256 / LANES;
+  if (flight > kRouteThreads<NE> / LANES) flight = kRouteThreads<NE> / LANES;
   if (flight < 1) flight = 1;
   while (flight > 1 && fixed + flight * token_bytes > 64 * 1024) flight /= 2;
   int threads = (int)((flight * LANES + 63) / 64 * 64);
@@ -449,7 +524,7 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
   else if (a.E <= 32) launch_route<16, 2>(a, per, chunks, stream);
   else if (a.E <= 64) launch_route<16, 4>(a, per, chunks, stream);
   else if (a.E <= 128) launch_route<16, 8>(a, per, chunks, stream);
-  else if (a.E <= 256) launch_route<16, 16>(a, per, chunks, stream);
+  else if (a.E <= 256) launch_route<32, 8>(a, per, chunks, stream);
   else if (a.E <= 512) launch_route<64, 8>(a, per, chunks, stream);
   else launch_route<64, 16>(a, per, chunks, stream);
   const hipError_t e = hipGetLastError();
