@@ -85,9 +85,15 @@ def stages(K: int) -> int:
     return (K + 127) // 128
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:  # an import statement on every call would cost what a check does
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(device) -> int:
@@ -741,13 +747,19 @@ def unpack_stage_major(codes, scales, K: int):
 def _check_mx(t, name, ndim=3):
     """An MXFP4 tensor's codes and scales are contiguous, stage-major and fit its K."""
     torch = _torch()
-    codes, scales = t.codes, t.scales
+    codes, scales, G = t.codes, t.scales, stages(t.K)
+    if type(codes) is type(scales) is torch.Tensor:
+        shape, sshape = codes.shape, scales.shape
+        if (codes.dtype is scales.dtype is torch.uint8 and codes.is_cuda and scales.is_cuda and len(shape) == ndim
+                and shape[-3] == G and shape[-1] == 64 and sshape[:-1] == shape[:-1] and sshape[-1] == 4
+                and codes.is_contiguous() and scales.is_contiguous()):
+            return
     _need(codes, torch.uint8, name + ".codes", ndim)
     _need(scales, torch.uint8, name + ".scales", ndim)
     shape, sshape = codes.shape, scales.shape
-    if shape[-3] != stages(t.K) or shape[-1] != 64 or sshape[:-1] != shape[:-1] or sshape[-1] != 4:
-        raise ValueError(f"{name}: expected stage-major codes [.., {stages(t.K)}, R, 64] and scales "
-                         f"[.., {stages(t.K)}, R, 4], got {tuple(shape)} and {tuple(sshape)}")
+    if shape[-3] != G or shape[-1] != 64 or sshape[:-1] != shape[:-1] or sshape[-1] != 4:
+        raise ValueError(f"{name}: expected stage-major codes [.., {G}, R, 64] and scales [.., {G}, R, 4], "
+                         f"got {tuple(shape)} and {tuple(sshape)}")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous")
 

@@ -471,7 +471,7 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs a, int64_t chu
   if (part < parts)
     for (int e = tid - part * width; e < a.E; e += width) {
       int sum = 0, pre = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int r = part; r < chunks; r += parts) {
         const int v = a.counts[(int64_t)r * a.E + e];
         sum += v;
@@ -529,8 +529,7 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
   else launch_route<64, 16>(a, per, chunks, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks == 1) return e;
-  const int threads = per * a.k >= 512 || a.E >= 512 ? 1024 : 512;
-  hipLaunchKernelGGL(moe_plan_kernel, dim3(chunks), dim3(threads), 16 * (size_t)a.E, stream, a, per, chunks);
+  hipLaunchKernelGGL(moe_plan_kernel, dim3(chunks), dim3(1024), 16 * (size_t)a.E, stream, a, per, chunks);
   return hipGetLastError();
 }
 

@@ -399,10 +399,8 @@ bool mx_aligned(const sharq::MxProduct& m) {
   return aligned16(m.a_codes) && aligned16(m.a_scales) && aligned16(m.w_codes) && aligned16(m.w_scales);
 }
 
-// Workgroups of a dense product's grid (32-row tiles at most below 33 rows).
-bool mx_grid_ok(int64_t T, int64_t O) {
-  return ((T + 127) / 128) * ((O + 255) / 256) * 16 <= kMaxGroupedTiles;  // 16: the largest K split
-}
+// Workgroups of a dense product's grid: one row tile up to 128 rows, 16 the largest K split.
+bool mx_grid_ok(int64_t T, int64_t O) { return ((T + 127) / 128) * ((O + 255) / 256) * 16 < kMaxGroupedTiles; }
 
 int check_workspace(const void* workspace, int64_t bytes) {
   if (bytes < 0 || (bytes > 0 && !workspace)) return SHARQ_EINVAL;
@@ -457,7 +455,7 @@ int check_mx_grouped(const sharq::MxProduct& m, const int32_t* a_rows, const int
   const int rc = check_mx(m.rows, m.O, m.K);
   if (rc != SHARQ_OK) return rc;
   if (E < 1 || P < 0 || P >= ((int64_t)1 << 31) || (!a_rows && m.rows < P)) return SHARQ_EINVAL;
-  if (sharq::mx_grouped_workgroups(P, E, tiles_n) > kMaxGroupedTiles) return SHARQ_EINVAL;
+  if (sharq::mx_grouped_workgroups(P, E, tiles_n) >= kMaxGroupedTiles) return SHARQ_EINVAL;
   if (P == 0 || m.O == 0) return SHARQ_OK;
   if (mx_null(m) || !seg_offsets) return SHARQ_EINVAL;
   if (!mx_aligned(m) || ((uintptr_t)seg_offsets & 3u) || ((uintptr_t)a_rows & 3u)) return SHARQ_EALIGN;

@@ -526,7 +526,7 @@ SHARQ_API int sharq_quantize_mxfp4_rms(const uint16_t* x, int64_t T, int64_t K, 
  *     in time need separate workspaces.
  * Accumulation is fp32 in an order that depends on the shape (and on whether
  * K was split) only, so calls are deterministic. Requires K % 32 == 0,
- * T, O < 2^25, ceil(T/128) * ceil(O/256) <= 2^20.
+ * T, O < 2^25, ceil(T/128) * ceil(O/256) < 2^20.
  */
 SHARQ_API int64_t sharq_linear_mxfp4_workspace_bytes(int64_t T, int64_t O, int64_t K);
 SHARQ_API int sharq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
@@ -560,9 +560,10 @@ SHARQ_API int sharq_linear_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_s
  *  u8 [E][G][O][4] (O = 2 I for the fused form);
  *  y [P][O] of type dtype; h_codes u8 [ceil(I/128)][P][64], h_scales.
  * Malformed segment or gather contents are handled as sharq_linear_grouped
- * does. Requires T_src, O < 2^25 (P < 2^25 for the fused form) and at most
- * 2^24 workgroups: (ceil(P / rows) + E) * ceil(O / 256), rows = 32 for
- * P <= 16 E, 64 for P <= 64 E, else 128.
+ * does. seg_offsets and a_rows need 4-byte alignment only. Requires T_src, O <
+ * 2^25 (P < 2^25 for the fused form) and fewer than 2^24 workgroups:
+ * (ceil(P / rows) + E) * ceil(O / 256), rows = 32 for P <= 16 E, 64 for P <=
+ * 64 E, else 128 (O / 256: I / 128 for the fused form).
  */
 SHARQ_API int sharq_linear_grouped_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src,
                                const int32_t* a_rows, const int32_t* seg_offsets, int32_t E, const uint8_t* w_codes,
@@ -603,6 +604,7 @@ SHARQ_API int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint
  *          (what sharq_moe_combine reads).
  *  workspace  at least sharq_moe_route_workspace_bytes(T, E) bytes, 16-byte
  *          aligned (may be 0 and NULL for T <= 64); overwritten.
+ * The logits need the alignment of their type, the other arrays 4 bytes.
  * T = 0 writes seg_offsets only. Requires 1 <= k <= E / groups * top_groups,
  * E % groups == 0, T k < 2^31; E <= 1024 and k <= 64 (SHARQ_ENOTIMPL).
  */

@@ -182,6 +182,39 @@ def test_captured_with_a_changing_token_count(sq, T):
         check(sq.moe_route(x, k, num_tokens=n), moe_route_ref(logits, k, num_tokens=live))
 
 
+@pytest.mark.parametrize("T,k", [(1, 3), (7, 3), (40, 2)])
+def test_feeds_the_two_path_grouped_calls(sq, T, k):
+    """The plan is what linear_grouped, linear_grouped_silu_prepare and moe_combine of fp32 rows read (with an odd
+    number of pairs too); a padded batch leaves the rows behind its pairs alone and combines them to zero."""
+    import torch
+    from oracle import linear_grouped_ref, moe_combine_ref, prepare_ref, quantize_weight_ref
+    from synth import bf16_round
+    from gpu_util import assert_y_close, bf16_to_gpu, oracle_prepared, w_to_gpu
+    rng = np.random.default_rng(T)
+    E, K, O = 5, 128, 256
+    x = bf16_round(rng.standard_normal((T, K)).astype(np.float32))
+    wq = [quantize_weight_ref(bf16_round((rng.standard_normal((O, K)) * 0.1).astype(np.float32))) for _ in range(E)]
+    wc, ws = np.stack([c for c, _ in wq]), np.stack([s for _, s in wq])
+    logits = rng.standard_normal((T + 3, E)).astype(np.float32)
+    r = sq.moe_route(f32_to_gpu(logits), k, num_tokens=i32_to_gpu([T]))
+    ref = moe_route_ref(logits, k, num_tokens=T)
+    check(r, ref)
+    p = prepare_ref(x, None, 2, 4)
+    P = (T + 3) * k
+    y = torch.full((P, O), 7.0, device="cuda")
+    sq.linear_grouped(oracle_prepared(p), w_to_gpu(wc, ws), r.seg_offsets, r.a_rows, out=y)
+    n = int(ref["seg_offsets"][-1])
+    want, bound = linear_grouped_ref(p["bb_codes"], p["bb_scales"], p["res_codes"], p["res_scales"],
+                                     ref["a_rows"][:n], ref["seg_offsets"], wc, ws)
+    assert_y_close(to_np(y)[:n], want, bound)
+    assert (y[n:] == 7).all()
+    hp, _ = sq.linear_grouped_silu_prepare(oracle_prepared(p), w_to_gpu(wc, ws), r.seg_offsets, r.a_rows)
+    assert hp.K == O // 2
+    out = to_np(sq.moe_combine(y, r.pair_index, r.weight))
+    full, fb = moe_combine_ref(to_np(y), ref["pair_index"], to_np(r.weight))
+    assert np.all(np.abs(out - full) <= k * 2.0 ** -24 * fb + 2.0 ** -126) and (out[T:] == 0).all()
+
+
 def test_refusals(sq):
     import torch
     x = torch.zeros((4, 12), device="cuda")
