@@ -99,20 +99,38 @@ __device__ __forceinline__ float load_logit(const void* x, int dtype, int64_t i)
 }
 
 // NE logits of a row from expert e0 on; -inf for what cannot be chosen (no such
-// expert, a padding row, -inf or NaN), +inf as the largest finite value.
+// expert, a padding row, -inf or NaN), +inf as the largest finite value. wide:
+// rows are 16-byte aligned and a lane's experts are all there or all not.
+template <class T>
+__device__ __forceinline__ float widen(T v) {
+  if constexpr (std::is_same<T, uint16_t>::value) return __uint_as_float((uint32_t)v << 16);
+  else return (float)v;
+}
 template <int NE, class T>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int e0, int E, bool live, float (&x)[NE]) {
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int e0, int E, bool live, bool wide,
+                                         float (&x)[NE]) {
+  constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    float v = -__builtin_huge_valf();
-    if (live && e0 + i < E) {
-      if constexpr (std::is_same<T, uint16_t>::value)
-        v = __uint_as_float((uint32_t)row[e0 + i] << 16);
-      else
-        v = (float)row[e0 + i];
+  for (int i = 0; i < NE; ++i) x[i] = -__builtin_huge_valf();
+  if constexpr (NE % kPer == 0) {
+    if (wide && live && e0 < E) {
+      uint4 raw[NE / kPer];
+#pragma unroll
+      for (int q = 0; q < NE / kPer; ++q) raw[q] = reinterpret_cast<const uint4*>(row + e0)[q];
+      T v[NE];
+      __builtin_memcpy(v, raw, sizeof(v));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) x[i] = widen(v[i]);
     }
-    x[i] = v > -__builtin_huge_valf() ? fminf(v, 3.4028234663852886e38f) : -__builtin_huge_valf();
   }
+  if (NE % kPer != 0 || !wide) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (live && e0 + i < E) x[i] = widen(row[e0 + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    x[i] = x[i] > -__builtin_huge_valf() ? fminf(x[i], 3.4028234663852886e38f) : -__builtin_huge_valf();
 }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
@@ -268,7 +286,9 @@ __device__ __forceinline__ float score_inverse(float x) { return __builtin_amdgc
 // e / sum of at most 21 rounded additions of terms off by a mean of at most
 // (2.5 ln 1024 + 2) u: p (2.5 |y| + 2 + 21 + 20 + 3) u < 3.5e-6 / sum, as p <=
 // 1 / sum and p |y| < 0.37 / sum. Adding the bias rounds by u of the result.
-// Two values closer than twice the bound are taken for close.
+// A key drops log2(NE) bits for the number of its register. Two values that
+// follow each other in the order (the first left out among them) and are
+// closer than twice all that are taken for close.
 template <int LANES, int NE, bool kBias, class V>
 __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE], int lane, int* chosen,
                                        double* gbuf) {
@@ -310,6 +330,7 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
   for (int i = 0; i < NE; ++i) {
     const V v = kBias ? value[i] : (V)x[i];
     key[i] = v > (V)kNegInf ? ordered(v) : 0;
+    if constexpr (kRough) key[i] = key[i] ? (key[i] & ~(Key)(NE - 1)) | (NE - 1 - i) : 0;  // says its register
   }
   if (a.groups > 1) {
     V near = -1;
@@ -324,33 +345,34 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
   }
   for (int j = lt; j < a.k; j += LANES) chosen[j] = -1;
   wave_sync();
-  // this lane's token in a ballot: the lanes below it, and all of them
+  // the lanes of this lane's token below it, in a half of a ballot
   const uint32_t shift = lane & 31 & ~(LANES - 1);
   const uint32_t below = ((1u << (lt & 31)) - 1u) << shift;
-  const uint32_t whole = (LANES >= 32 ? 0xFFFFFFFFu : (1u << (LANES & 31)) - 1u) << shift;
   auto lanes_of = [&](uint64_t m) { return lane < 32 ? (uint32_t)m : (uint32_t)(m >> 32); };
-  for (int j = 0; j < a.k; ++j) {
+  float last = 0.0f;
+  for (int j = 0; j < a.k + (kRough ? 1 : 0); ++j) {
     Key head = key[0];
 #pragma unroll
     for (int i = 1; i < NE; ++i) head = max(head, key[i]);
     const Key best = token_reduce<LANES>(head, [](Key p, Key q) { return max(p, q); });
+    if constexpr (kRough) {  // the one before, and this one: far enough apart to tell? (NaN, of infinities, is not)
+      const float v = __uint_as_float((uint32_t)(best >> 31 ? best ^ 0x80000000u : ~best));
+      const float rounding = (float)(NE + 1) * 1.2e-7f * fmaxf(fabsf(v), fabsf(last));
+      close |= j > 0 && best != 0 && !(last - v > 2.0f * ((float)bound + rounding));
+      last = v;
+      if (j == a.k) break;
+    }
     const bool has = head == best && best != 0;
     const uint64_t have = __ballot(has);
-    if constexpr (kRough) {  // keys from `low` on are too near the best to tell
-      const float v = __uint_as_float((uint32_t)(best >> 31 ? best ^ 0x80000000u : ~best));
-      const Key low = best ? ordered(v - 2.0f * ((float)bound + fabsf(v) * 1.2e-7f)) : 1;
-      int same = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) same += key[i] >= low;
-      const uint64_t near = __ballot(same > 0);
-      const int lanes = LANES == 64 ? __popcll(near) : __popc(lanes_of(near) & whole);
-      close |= best != 0 && (same > 1 || lanes > 1);
-    }
     const bool first = LANES == 64 ? (have & ((1ull << lt) - 1)) == 0 : (lanes_of(have) & below) == 0;
     int at = -1;
+    if constexpr (kRough) {
+      if (has && first) at = NE - 1 - (int)(best & (NE - 1));
+    } else {
 #pragma unroll
-    for (int i = NE - 1; i >= 0; --i) at = key[i] == best ? i : at;
-    if (!(has && first)) at = -1;
+      for (int i = NE - 1; i >= 0; --i) at = key[i] == best ? i : at;
+      if (!(has && first)) at = -1;
+    }
     if (at >= 0) chosen[j] = lt * NE + at;
 #pragma unroll
     for (int i = 0; i < NE; ++i) key[i] = at == i ? 0 : key[i];
@@ -391,9 +413,11 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
     const bool row = t < t1 && t < live_rows;
     float x[NE];
     const int64_t at_row = row ? t * a.ld : 0;
-    if (a.dtype == 0) load_row<NE>(static_cast<const float*>(a.logits) + at_row, lt * NE, a.E, row, x);
-    else if (a.dtype == 1) load_row<NE>(static_cast<const uint16_t*>(a.logits) + at_row, lt * NE, a.E, row, x);
-    else load_row<NE>(static_cast<const _Float16*>(a.logits) + at_row, lt * NE, a.E, row, x);
+    const int item = a.dtype == 0 ? 4 : 2;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.logits) | (uintptr_t)(a.ld * item)) & 15) == 0 && a.E % NE == 0;
+    if (a.dtype == 0) load_row<NE>(static_cast<const float*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
+    else if (a.dtype == 1) load_row<NE>(static_cast<const uint16_t*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
+    else load_row<NE>(static_cast<const _Float16*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
     if (select<LANES, NE, kBias, float>(a, x, lane, chosen, gbuf))
       select<LANES, NE, kBias, double>(a, x, lane, chosen, gbuf);
     double ref = 0.0, total = 1.0;  // softmax: the row's largest logit, and the sum of exp(x - ref)
