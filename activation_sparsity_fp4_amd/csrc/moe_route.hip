@@ -206,11 +206,8 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Doubles of LDS that the groups of a token take: its values (or the two
-// largest of each lane) and the groups' scores.
-__host__ __device__ constexpr int group_doubles(int E, int groups, int lanes) {
-  return (E > 2 * lanes ? E : 2 * lanes) + groups;
-}
+// Doubles of LDS that the groups of a token take: its values, the groups' scores and which are kept.
+__host__ __device__ constexpr int group_doubles(int E, int groups) { return E + groups + (groups + 1) / 2; }
 
 template <class V>
 __device__ __forceinline__ void take_two(V v, V& first, V& second) {
@@ -227,43 +224,50 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, const V (&v)[NE]
                                             V near) {
   const int size = a.E / a.groups;
   V* buf = reinterpret_cast<V*>(lds);
-  V* gscore = buf + group_doubles(a.E, 0, LANES);
-  const bool whole = size % NE == 0;  // a lane's experts belong to one group
-  if (whole) {
+  V* gscore = buf + a.E;
+  int* kept = reinterpret_cast<int*>(lds + a.E + a.groups);
+  const int lanes = size / NE;  // lanes of a group, where a lane's experts belong to one
+  if (size % NE == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LANES) {
+    // the two largest of each lane, then of the aligned lanes of a group
     V first = kNegInf, second = kNegInf;
 #pragma unroll
     for (int i = 0; i < NE; ++i) take_two<V>(v[i], first, second);
-    buf[2 * lt] = first;
-    buf[2 * lt + 1] = second;
+    for (int d = 1; d < lanes; d <<= 1) {
+      const V f = __shfl_xor(first, d, 64), s = __shfl_xor(second, d, 64);
+      second = max(min(first, f), max(second, s));
+      first = max(first, f);
+    }
+    if (lt % lanes == 0 && lt / lanes < a.groups)
+      gscore[lt / lanes] = first + (a.sum2 && second > (V)kNegInf ? second : (V)0);
   } else {
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (lt * NE + i < a.E) buf[lt * NE + i] = v[i];
+    wave_sync();
+    for (int g = lt; g < a.groups; g += LANES) {
+      V first = kNegInf, second = kNegInf;
+      for (int e = g * size; e < (g + 1) * size; ++e) take_two<V>(buf[e], first, second);
+      gscore[g] = first + (a.sum2 && second > (V)kNegInf ? second : (V)0);
+    }
   }
   wave_sync();
-  const int per = whole ? 2 * (size / NE) : size;  // entries of a group
+  bool close = false;
   for (int g = lt; g < a.groups; g += LANES) {
-    V first = kNegInf, second = kNegInf;
-    for (int e = g * per; e < (g + 1) * per; ++e) take_two<V>(buf[e], first, second);
-    gscore[g] = first + (a.sum2 && second > (V)kNegInf ? second : (V)0);
+    const V mine = gscore[g];
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < a.groups; ++o) {
+      const V other = gscore[o];
+      rank += other > mine || (other == mine && o < g);
+      close |= o != g && fabs(other - mine) <= near;
+    }
+    kept[g] = rank < a.top_groups;
   }
   wave_sync();
-  int g = lt * NE / size, in = lt * NE - g * size, seen = -1;
-  bool keep = false, close = false;
+  int g = lt * NE / size, in = lt * NE - g * size;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    if (g != seen && g < a.groups) {
-      const V mine = gscore[g];
-      int rank = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        const V other = gscore[o];
-        rank += other > mine || (other == mine && o < g);
-        close |= o != g && fabs(other - mine) <= near;
-      }
-      keep = rank < a.top_groups;
-      seen = g;
-    }
-    if (!keep) key[i] = 0;
+    if (kept[min(g, a.groups - 1)] == 0) key[i] = 0;
     if (++in == size) in = 0, ++g;
   }
   wave_sync();
@@ -401,7 +405,7 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
   int* before = counts + a.E;
   int* chosen = before + a.E + (int64_t)slot * a.k;
   double* gbuf = reinterpret_cast<double*>(before + a.E + ((int64_t)flight * a.k + 1) / 2 * 2) +
-                 (int64_t)slot * group_doubles(a.E, a.groups, LANES);
+                 (int64_t)slot * group_doubles(a.E, a.groups);
   for (int e = tid; e < a.E; e += blockDim.x) counts[e] = 0, before[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * chunk_tokens;
@@ -520,7 +524,7 @@ int64_t chunk_tokens(int64_t T) {
 template <int LANES, int NE>
 void launch_route(const RouteArgs& a, int64_t per, int chunks, hipStream_t stream) {
   // tokens in flight: the chunk's, at most a workgroup's worth and 64 KB of LDS
-  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups, LANES) : 0);
+  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups) : 0);
   const int64_t fixed = 16 * (int64_t)a.E + 8;  // 8: the groups' doubles are aligned
   int64_t flight = (a.T < per ? a.T : per);
   if (flight > kRouteThreads<NE> / LANES) flight = kRouteThreads<NE> / LANES;
