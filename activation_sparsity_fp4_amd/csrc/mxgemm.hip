@@ -65,15 +65,15 @@ struct MxOperands {
   int nsteps;
 };
 
-// Scale loads of a wave in a stage, 16 bytes a lane: even waves the weight's
-// 256 dwords, odd waves the activation's (waves beyond the second repeat a
-// load, the same bytes to the same place, so that all waves count alike). When
-// rows are gathered: the weight's, and one 64-row run of the activation's with
-// a dword a lane. (Into LDS, a dword a lane holds the CU's load path for 32
-// cycles, 16 bytes a lane for 16. 16 bytes partly outside the view read zeros
-// per dword.)
-template <class C, bool kGather>
-constexpr int kLoads = C::kCodeLoads + (kGather ? 2 : 1);
+// A wave has one scale load in a stage (waves that share one load the same
+// bytes to the same place, so that all waves count alike). Into LDS, a dword a
+// lane holds the CU's load path for 32 cycles, 16 bytes a lane for 16, so that
+// is the form wherever rows lie side by side: even waves load the weight's 256
+// dwords, odd waves the activation's. (16 bytes partly outside the view read
+// zeros per dword.) Gathered activation rows take a dword a lane: the first
+// waves load a 64-row run each, the others the weight's dwords.
+template <class C>
+constexpr int kLoads = C::kCodeLoads + 1;
 
 template <class C>
 struct MxFrags {
@@ -140,15 +140,14 @@ __device__ __forceinline__ void mx_shift_scales(MxScales<C>& c, uint32_t bits) {
   for (int j = 0; j < C::WN; ++j) asm volatile("v_lshrrev_b32 %0, %1, %0" : "+v"(c.w[j]) : "v"(bits));
 }
 
-// MFMA number M of a sub-step. kSkip: row blocks from `active` on hold no
-// valid row (a partial last tile of an expert segment) and are skipped.
-template <class C, int SUB, int M, bool kSkip>
-__device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
-                                        int active) {
+// MFMA number M of a sub-step. (Skipping the row blocks of a partial expert
+// tile that hold no valid row puts a branch at every MFMA: the grouped gate|up
+// of the Qwen3-30B-A3B layer 92.8 us with it, 89.4 without.)
+template <class C, int SUB, int M>
+__device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN]) {
   constexpr int i = M / C::WN, j = M % C::WN;
-  if (!kSkip || i < active)
-    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[j], f.a[i], acc[i][j], 4, 4, 2 * SUB,
-                                                                (int)c.w[j], 2 * SUB, (int)c.a[i]);
+  acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.w[j], f.a[i], acc[i][j], 4, 4, 2 * SUB,
+                                                              (int)c.w[j], 2 * SUB, (int)c.a[i]);
 }
 
 // Buffer loads into LDS as in gemm_common.h, the LDS address a sum formed in
@@ -158,9 +157,9 @@ __device__ __forceinline__ void load_lds16(i32x4 rsrc, uint32_t voff, uint32_t b
   asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(base), "n"(BYTES) : "memory", "m0", "scc");
 }
-__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t base, uint32_t bytes) {
-  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(base), "s"(bytes) : "memory", "m0", "scc");
+__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(base) : "memory", "m0");
 }
 
 // One operand array: the buffer view of the stage to load next.
@@ -180,22 +179,21 @@ struct MxView {
   }
 };
 
-// The loads of a wave. Every array's view moves on right behind its last load
+// The loads of a wave; kDword: its scale load is a dword a lane. Every array's view moves on right behind its last load
 // of a stage, so that the scalar work is spread between the MFMAs too.
-template <class C, bool kGather>
+template <class C, bool kDword>
 struct MxLoader {
-  MxView a, w, s, g;            // codes; the wave's 16-byte scale load; gathered activation scales
+  MxView a, w, s;               // codes; the scales that the wave loads
   uint32_t a_off[C::kAChunks];  // byte offset of this lane's A code chunk inside a stage, kOOB if absent
   uint32_t w_off[C::kWChunks];
-  uint32_t s_off, g_off;        // this lane's scale dwords
+  uint32_t s_off;               // this lane's scale dwords
   uint32_t wave_base;           // 1024 * wave: the wave's chunk inside a stage
-  uint32_t s_lds, g_lds;        // where its scales go inside a stage
+  uint32_t s_lds;               // where its scales go inside a stage
   uint32_t ring, at;            // LDS address of the ring; offset of the slot to fill
   int left;                     // stages not yet issued; batches past the last one read nothing
 
   template <int J>
   __device__ __forceinline__ void issue() {
-    constexpr int kN = kLoads<C, kGather>;
     if constexpr (J < C::kAChunks) {
       load_lds16<C::kOffA + 1024 * C::kWaves * J>(a.r, a_off[J], ring + at + wave_base);
       if constexpr (J == C::kAChunks - 1) a.advance(--left > 0);
@@ -203,14 +201,14 @@ struct MxLoader {
       constexpr int j = J - C::kAChunks;
       load_lds16<C::kOffW + 1024 * C::kWaves * j>(w.r, w_off[j], ring + at + wave_base);
       if constexpr (J == C::kCodeLoads - 1) w.advance(left > 0);
-    } else if constexpr (J == C::kCodeLoads) {
-      load_lds16<0>(s.r, s_off, ring + at + s_lds);
+    } else {
+      if constexpr (kDword)
+        load_lds4(s.r, s_off, ring + at + s_lds);
+      else
+        load_lds16<0>(s.r, s_off, ring + at + s_lds);
       s.advance(left > 0);
-    } else if constexpr (J < kN) {
-      load_lds4(g.r, g_off, ring + at, g_lds);
-      g.advance(left > 0);
+      at = at + C::kStage == C::kRing * C::kStage ? 0 : at + C::kStage;
     }
-    if constexpr (J == kN - 1) at = at + C::kStage == C::kRing * C::kStage ? 0 : at + C::kStage;
   }
   template <int J, int END>
   __device__ __forceinline__ void issue_range() {
@@ -221,7 +219,7 @@ struct MxLoader {
   }
   // Loads of slots [0, SLOT) of the 2 kHalf slots over which a stage's are spread.
   template <int SLOT>
-  static constexpr int kBefore = (SLOT * kLoads<C, kGather> + 2 * C::kHalf - 1) / (2 * C::kHalf);
+  static constexpr int kBefore = (SLOT * kLoads<C> + 2 * C::kHalf - 1) / (2 * C::kHalf);
   template <int FROM, int TO>
   __device__ __forceinline__ void issue_slots() {
     issue_range<kBefore<FROM>, kBefore<TO>>();
@@ -240,61 +238,47 @@ struct MxLoader {
 // second half and the first half of the next iteration: the waves of a barrier
 // that issue theirs in a burst queue up at the CU's one load path (16 cycles a
 // KB), and an MFMA behind a queued load waits with it.
-template <class C, int M, bool kSkip>
+template <class C, int M, bool kDword>
 __device__ __forceinline__ void mx_first_half(const MxFrags<C>& f0, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
-                                              MxLoader<C, kSkip>& ld, const uint8_t* cur,
-                                              MxFrags<C>& f1, MxScales<C>& unused, int wm, int wn, int lr, int lh,
-                                              int active) {
+                                              MxLoader<C, kDword>& ld, const uint8_t* cur,
+                                              MxFrags<C>& f1, MxScales<C>& unused, int wm, int wn, int lr, int lh) {
   if constexpr (M < C::kHalf) {
-    mx_mfma<C, 0, M, kSkip>(f0, c, acc, active);
+    mx_mfma<C, 0, M>(f0, c, acc);
     mx_read_range<C, 1, M * kReadsPerSlot<C>, (M + 1) * kReadsPerSlot<C>>(cur, f1, unused, wm, wn, lr, lh);
     ld.template issue_slots<C::kHalf + M, C::kHalf + M + 1>();
     __builtin_amdgcn_sched_barrier(0);
-    mx_first_half<C, M + 1, kSkip>(f0, c, acc, ld, cur, f1, unused, wm, wn, lr, lh, active);
+    mx_first_half<C, M + 1, kDword>(f0, c, acc, ld, cur, f1, unused, wm, wn, lr, lh);
   }
 }
 
-template <class C, int M, bool kSkip>
+template <class C, int M, bool kDword>
 __device__ __forceinline__ void mx_second_half(const MxFrags<C>& f1, const MxScales<C>& c, v16f (&acc)[C::WM][C::WN],
-                                               MxLoader<C, kSkip>& ld, const uint8_t* next,
-                                               MxFrags<C>& f0, MxScales<C>& cn, int wm, int wn, int lr, int lh,
-                                               int active) {
+                                               MxLoader<C, kDword>& ld, const uint8_t* next,
+                                               MxFrags<C>& f0, MxScales<C>& cn, int wm, int wn, int lr, int lh) {
   if constexpr (M < C::kHalf) {
-    mx_mfma<C, 1, M, kSkip>(f1, c, acc, active);
+    mx_mfma<C, 1, M>(f1, c, acc);
     mx_read_range<C, 0, M * kReadsPerSlot<C>, (M + 1) * kReadsPerSlot<C>>(next, f0, cn, wm, wn, lr, lh);
     if constexpr (M == C::kHalf - 1) mx_shift_scales<C>(cn, 8 * lh);
     ld.template issue_slots<M, M + 1>();
     __builtin_amdgcn_sched_barrier(0);
-    mx_second_half<C, M + 1, kSkip>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh, active);
+    mx_second_half<C, M + 1, kDword>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh);
   }
 }
 
-// acc += the product over stages [s_begin, s_end) (s_begin < s_end).
-template <class C, bool kSkip>
-__device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows& tr, const TileCols& tc,
-                                            uint8_t* ring, v16f (&acc)[C::WM][C::WN], int s_begin, int s_end) {
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+template <class C, bool kDword>
+__device__ __forceinline__ void mx_loop(const MxOperands& op, const TileRows& tr, const TileCols& tc,
+                                        uint8_t* ring, v16f (&acc)[C::WM][C::WN], int s_begin, int s_end, int wave,
+                                        bool act_scales) {
+  const int lane = threadIdx.x & 63;
   const int wm = wave % C::NWM, wn = wave / C::NWM;
   const int lr = lane & 31, lh = lane >> 5;
-  const int64_t first_row = 32 * C::WM * wm;
-  const int active = __builtin_amdgcn_readfirstlane(
-      !kSkip ? C::WM
-      : tr.rows_valid <= first_row ? 0
-      : (int)min<int64_t>((tr.rows_valid - first_row + 31) / 32, C::WM));
-
-  MxLoader<C, kSkip> ld;
-  constexpr int kARuns = (C::BM + 63) / 64;
-  const bool act_scales = !kSkip && (wave & 1);
+  MxLoader<C, kDword> ld;
   ld.left = s_end - s_begin;
   ld.a.start(op.a_codes, op.rows * kRowBytes, s_begin);
   ld.w.start(op.w_codes, op.O * kRowBytes, s_begin);
   ld.s.start(act_scales ? op.a_scales : op.w_scales, (act_scales ? op.rows : op.O) * 4, s_begin);
-  if (kSkip) ld.g.start(op.a_scales, op.rows * 4, s_begin);
   ld.wave_base = 1024 * wave;
-  ld.s_lds = act_scales ? C::kOffSA : C::kOffSW;
-  ld.g_lds = C::kOffSA + 256 * (wave % kARuns);
+  ld.s_lds = kDword ? C::kOffSA + 256 * wave : act_scales ? C::kOffSA : C::kOffSW;
   ld.ring = lds_offset(ring);
   ld.at = 0;
   // A lane fills a fixed LDS chunk; it reads the global chunk that belongs there after the swizzle.
@@ -310,24 +294,23 @@ __device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows
     const int64_t o = tc.w_row(row);
     ld.w_off[j] = o < op.O ? (uint32_t)(o * kRowBytes + ((lane & 3) ^ swz_part(row)) * 16) : kOOB;
   }
-  ld.s_off = ld.g_off = kOOB;
-  if (!act_scales) {
+  ld.s_off = kOOB;
+  if (kDword) {
+    const int64_t src = tr.src(64 * wave + lane);
+    if (src >= 0) ld.s_off = (uint32_t)(src * 4);
+  } else if (!act_scales) {
     const int64_t o = tc.w_row(4 * lane);  // four rows of one 64-row block
     if (o < op.O) ld.s_off = (uint32_t)(o * 4);
   } else if (4 * lane < C::BM && tr.m0 + 4 * lane < op.rows) {
     ld.s_off = (uint32_t)((tr.m0 + 4 * lane) * 4);
   }
-  if (kSkip) {
-    const int64_t src = tr.src(64 * (wave % kARuns) + lane);
-    if (src >= 0) ld.g_off = (uint32_t)(src * 4);
-  }
 
   // The first ring of stages; the last one's first-half loads follow in the loop.
-  constexpr int kN = kLoads<C, kSkip>;
+  constexpr int kN = kLoads<C>;
 #pragma unroll
   for (int b = 0; b + 1 < C::kRing; ++b) ld.template issue_range<0, kN>();
   ld.template issue_slots<0, C::kHalf>();
-  wait_vmcnt<(C::kRing - 2) * kN + MxLoader<C, kSkip>::template kBefore<C::kHalf>>();  // the first batch landed
+  wait_vmcnt<(C::kRing - 2) * kN + MxLoader<C, kDword>::template kBefore<C::kHalf>>();  // the first batch landed
   ring_barrier();
   MxFrags<C> f0, f1;
   MxScales<C> c, cn;
@@ -339,18 +322,38 @@ __device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows
     const uint8_t* next = cur == ring + (C::kRing - 1) * C::kStage ? ring : cur + C::kStage;
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
-    mx_first_half<C, 0, kSkip>(f0, c, acc, ld, cur, f1, cn, wm, wn, lr, lh, active);
+    mx_first_half<C, 0, kDword>(f0, c, acc, ld, cur, f1, cn, wm, wn, lr, lh);
     __builtin_amdgcn_s_setprio(0);
     wait_vmcnt<(C::kRing - 2) * kN>();  // the next stage landed; later batches may be in flight
     ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
-    mx_second_half<C, 0, kSkip>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh, active);
+    mx_second_half<C, 0, kDword>(f1, c, acc, ld, next, f0, cn, wm, wn, lr, lh);
     __builtin_amdgcn_s_setprio(0);
     c = cn;
     cur = next;
   }
   wait_vmcnt<0>();  // the trailing batches, before the LDS is used again
+}
+
+// acc += the product over stages [s_begin, s_end) (s_begin < s_end). The two
+// kinds of scale load are loops of their own, between which the waves of a
+// gathered tile part: a choice inside the loop would put branches between its
+// MFMAs, and with both loads in every wave two workgroups hold the CU's load
+// path for 1152 cycles a stage, longer than their MFMAs run (1024); this way
+// it is 960. Grouped gate|up, 4096 tokens x 8 of 128 experts, 2048 -> 2 x 768,
+// means of four runs in turn: 99 us with both, 94 so.
+template <class C, bool kGather>
+__device__ __forceinline__ void mx_mainloop(const MxOperands& op, const TileRows& tr, const TileCols& tc,
+                                            uint8_t* ring, v16f (&acc)[C::WM][C::WN], int s_begin, int s_end) {
+  constexpr int kARuns = (C::BM + 63) / 64;
+  static_assert(kARuns < C::kWaves, "a wave is left for the weight's scales");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool gathered = kGather && tr.gather != nullptr;
+  if (kGather && gathered && wave < kARuns)
+    mx_loop<C, true>(op, tr, tc, ring, acc, s_begin, s_end, wave, true);
+  else
+    mx_loop<C, false>(op, tr, tc, ring, acc, s_begin, s_end, wave, !gathered && (wave & 1));
 }
 
 template <class C>
