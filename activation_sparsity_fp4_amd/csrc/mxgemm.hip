@@ -619,7 +619,7 @@ __global__ __launch_bounds__(256) void mx_reduce_silu_kernel(const float* __rest
       if (q < S) gs += g[q], us += u[q];
     h = __uint_as_float(bf16_rne_bits(silu_times(gs, us)) << 16);
   }
-  float m = fabsf(h);
+  float m = fmaxf(0.0f, fabsf(h));  // 0 for NaN
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 32));
   const uint32_t byte = b < blocks ? e8m0_from_amax_bits(__float_as_uint(m)) : 0u;

@@ -377,7 +377,8 @@ __global__ __launch_bounds__(256) void quantize_rms_kernel(const uint16_t* __res
                                                            uint32_t rows, float eps, float* __restrict__ r_out,
                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   __shared__ double part[64];
-  const uint32_t t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const uint32_t t = blockIdx.y * gridDim.x + blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  if (t >= rows) return;  // uniform across the workgroup
   const uint32_t nb = K / kBlock, nblk_padded = (nb + 3) & ~3u, waves = blockDim.x >> 6;
   const uint16_t* xrow = x + (int64_t)t * ldx;
   uint4 held[kHold][4];
@@ -575,9 +576,11 @@ hipError_t launch_prepare(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, 
 hipError_t launch_quantize_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma, float eps,
                                float* rms_scale, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
   const unsigned threads = K <= 64 * kBlock ? 64 : K <= 128 * kBlock ? 128 : 256;
+  const int64_t gx = T < (1 << 20) ? T : 1 << 20;  // fewer than 2^32 threads along x
+  const dim3 grid((unsigned)gx, (unsigned)((T + gx - 1) / gx));
 #define SHARQ_QUANT_RMS(GG, HOLD)                                                                                   \
-  hipLaunchKernelGGL((quantize_rms_kernel<GG, HOLD>), dim3((unsigned)T), dim3(threads), 0, stream, x, ldx, gamma, \
-                     (uint32_t)K, (uint32_t)T, eps, rms_scale, codes, scales)
+  hipLaunchKernelGGL((quantize_rms_kernel<GG, HOLD>), grid, dim3(threads), 0, stream, x, ldx, gamma, (uint32_t)K, \
+                     (uint32_t)T, eps, rms_scale, codes, scales)
   if (K <= 256 * kBlock) {
     if (gamma) SHARQ_QUANT_RMS(true, 1); else SHARQ_QUANT_RMS(false, 1);
   } else {

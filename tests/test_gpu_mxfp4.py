@@ -404,3 +404,163 @@ def test_expert_layer(sq, T, E, k, H, I):
     out = sq.moe_combine(y, r.pair_index, r.weight)
     full, fb = moe_combine_ref(y.float().cpu().numpy(), ref["pair_index"], to_np(r.weight))
     assert np.all(np.abs(to_np(out) - full) <= k * 2.0 ** -24 * fb + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("T,K,I", [(5, 16384, 128), (40, 256, 96), (200, 544, 160)])
+def test_rows_without_a_number_stay_alone(sq, T, K, I):
+    """A row whose scales are NaN (0xFF) and one that overflows leave every other row as it is, and the fused forms
+    still equal their chains, codes of NaN included."""
+    import torch
+    print(f"NaN rows T={T} K={K} I={I}", flush=True)
+    rng = np.random.default_rng(T)
+    codes, scales = _rows(rng, T, K)
+    w = _mx(sq, _rows(rng, 2 * I, K, 0.05))
+    clean = _mx(sq, (codes, scales))
+    bad = scales.copy()
+    bad[1], bad[3, ::2] = 0xFF, 254
+    a = _mx(sq, (codes, bad))
+    keep = [t for t in range(T) if t not in (1, 3)]
+    for split in (True, False):
+        y = sq.linear_mxfp4(a, w, split_k=split)
+        assert torch.equal(y[keep], sq.linear_mxfp4(clean, w, split_k=split)[keep]) and y[1].isnan().all()
+        h = sq.linear_silu_mxfp4(a, w, split_k=split)
+        want = sq.quantize_mxfp4(sq.silu_mul(y))
+        assert torch.equal(h.scales, want.scales) and torch.equal(h.codes, want.codes)
+
+
+def _random_mx(sq, gen, *shape, K):
+    """Random codes and scales near 1, zeros where a partial last stage is padded."""
+    import torch
+    G, R = sq.stages(K), shape[-1]
+    codes = torch.randint(0, 256, (*shape[:-1], G, R, 64), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.randint(124, 128, (*shape[:-1], G, R, 4), dtype=torch.uint8, device="cuda", generator=gen)
+    left = K - 128 * (G - 1)
+    codes[..., G - 1, :, left // 2:] = 0
+    scales[..., G - 1, :, left // 32:] = 0
+    return sq.MXFP4(codes, scales, K)
+
+
+def _rows_of(sq, q, at):
+    return sq.MXFP4(q.codes[:, at].contiguous(), q.scales[:, at].contiguous(), q.K)
+
+
+def test_results_beyond_four_gigabytes(sq):
+    """Outputs, coded outputs and expert weights whose bytes pass 2^32: sampled rows equal those of small calls (the
+    additions of an element do not depend on the tile)."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    T = O = 33000
+    print("fp32 output", flush=True)
+    a, w = _random_mx(sq, gen, T, K=32), _random_mx(sq, gen, O, K=32)
+    at = torch.tensor([0, 31, T // 2, T - 129, T - 1], device="cuda")
+    y = sq.linear_mxfp4(a, w)
+    assert y.numel() * 4 > 1 << 32
+    assert torch.equal(y[at], sq.linear_mxfp4(_rows_of(sq, a, at), w, split_k=False))
+    del y
+    T, I = 1 << 20, 8224
+    print("coded output", flush=True)
+    a, w = _random_mx(sq, gen, T, K=32), _random_mx(sq, gen, 2 * I, K=32)
+    at = torch.tensor([0, 77, T // 2, T - 1], device="cuda")
+    h = sq.linear_silu_mxfp4(a, w)
+    assert h.codes.numel() > 1 << 32
+    want = sq.linear_silu_mxfp4(_rows_of(sq, a, at), w, split_k=False)
+    assert torch.equal(h.codes[:, at], want.codes) and torch.equal(h.scales[:, at], want.scales)
+    del h, a, w
+    E, O, K = 64, 131104, 1024
+    print("expert weights", flush=True)
+    a, w = _random_mx(sq, gen, 9, K=K), _random_mx(sq, gen, E, O, K=K)
+    assert w.codes.numel() > 1 << 32
+    seg = [0] + [2] * (E - 2) + [5, 9]  # expert 0, and the last two
+    y = sq.linear_grouped_mxfp4(a, w, i32_to_gpu(seg))
+    for e in (0, E - 2, E - 1):
+        one = sq.linear_mxfp4(a, sq.MXFP4(w.codes[e], w.scales[e], K), split_k=False)
+        assert torch.equal(y[seg[e]:seg[e + 1]], one[seg[e]:seg[e + 1]])
+    del y, w
+    P, H = 70000, 32768
+    print("combined rows", flush=True)
+    y = torch.randn(P, H, device="cuda", generator=gen, dtype=torch.bfloat16)
+    idx = torch.tensor([[P - 1, 0], [P - 2, -1]], dtype=torch.int32, device="cuda")
+    out = sq.moe_combine(y, idx, torch.tensor([[1.0, 0.0], [1.0, 1.0]], device="cuda"))
+    assert torch.equal(out, y[[P - 1, P - 2]].float())
+
+
+def test_norming_quantiser_of_many_rows(sq):
+    """More rows than one grid dimension holds workgroups for."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    T = (1 << 26) + 3
+    x = torch.randn(T, 32, device="cuda", generator=gen, dtype=torch.bfloat16)
+    at = torch.tensor([0, (1 << 20) - 1, 1 << 20, 1 << 26, T - 1], device="cuda")
+    print(f"{T} rows", flush=True)
+    q, want = sq.quantize_mxfp4(x, rms_eps=1e-5), sq.quantize_mxfp4(x[at], rms_eps=1e-5)
+    assert torch.equal(q.codes[:, at], want.codes) and torch.equal(q.scales[:, at], want.scales)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(40, 16, 4, 512, 96), (300, 6, 2, 256, 160)])
+def test_captured_expert_layer_of_padded_batches(sq, T, E, k, H, I):
+    """One graph of the whole expert layer serves batches of every fill. What lies behind the pairs is NaN: it is
+    left as it is and reaches no result."""
+    import torch
+    print(f"captured experts T={T} E={E}", flush=True)
+    rng = np.random.default_rng(T)
+    gu, dn = _mx(sq, _experts(rng, E, 2 * I, H)), _mx(sq, _experts(rng, E, H, I))
+    logits = f32_to_gpu(rng.standard_normal((T, E)).astype(np.float32))
+    x = bf16_to_gpu(bf16_round(rng.standard_normal((T, H)).astype(np.float32)))
+    h = sq.MXFP4(torch.empty((sq.stages(I), T * k, 64), dtype=torch.uint8, device="cuda"),
+                 torch.empty((sq.stages(I), T * k, 4), dtype=torch.uint8, device="cuda"), I)
+    y = torch.empty((T * k, H), dtype=torch.bfloat16, device="cuda")
+    n = i32_to_gpu([T])
+
+    def layer(logits, x, n=None, h=None, y=None):
+        r = sq.moe_route(logits, k, num_tokens=n)
+        h = sq.linear_grouped_silu_mxfp4(sq.quantize_mxfp4(x), gu, r.seg_offsets, r.a_rows, out=h)
+        y = sq.linear_grouped_mxfp4(h, dn, r.seg_offsets, out=y, dtype=torch.bfloat16)
+        return sq.moe_combine(y, r.pair_index, r.weight, bf16=True)
+
+    layer(logits, x, n, h, y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer(logits, x, n, h, y)
+    for live in (T, 1, 0, T // 3, T):
+        n.fill_(live)
+        h.codes.fill_(0xFF), h.scales.fill_(0xFF), y.fill_(float("nan")), out.fill_(float("nan"))
+        g.replay()
+        assert (out[live:] == 0).all() and y[live * k:].isnan().all() and (h.scales[:, live * k:] == 0xFF).all()
+        if live:
+            assert torch.equal(out[:live], layer(logits[:live], x[:live])), live
+
+
+@pytest.mark.parametrize("T,K", [(2, 16416), (3, 28672), (1, 131072)])
+def test_quantize_rms_of_long_rows(sq, T, K):
+    """Rows of more blocks than a workgroup holds in registers, up to the longest."""
+    print(f"quantize rms T={T} K={K}", flush=True)
+    rng = np.random.default_rng(K)
+    x = bf16_round((rng.standard_normal((T, K)) * rng.lognormal(0, 1, (T, 1))).astype(np.float32))
+    g = bf16_round(rng.uniform(0.5, 1.5, K).astype(np.float32))
+    xn, _ = rms_normalize_ref(x, 1e-5)
+    xp = (bf16_to_f32(xn) if xn.dtype == np.uint16 else np.asarray(xn, np.float32)) * bf16_to_f32(g)
+    codes, e = mxfp4_quantize(xp)
+    q = sq.quantize_mxfp4(bf16_to_gpu(x), gamma=bf16_to_gpu(g), rms_eps=1e-5)
+    assert np.array_equal(codes_row_major(to_np(q.codes), K // 2), pack_nibbles(codes))
+    assert np.array_equal(row_major(to_np(q.scales), K // 32), (e + 127).astype(np.uint8))
+
+
+def test_workspace_too_small_is_no_split(sq):
+    """At the C boundary a workspace below the asked size counts as none; a larger one splits."""
+    import torch
+    from activation_sparsity_fp4_amd import _lib
+    T, K, O = 2, 16384, 256
+    rng = np.random.default_rng(5)
+    a, w = _mx(sq, _rows(rng, T, K)), _mx(sq, _rows(rng, O, K))
+    need = _lib.call("sharq_linear_mxfp4_workspace_bytes", T, O, K)
+    assert need > 0
+    ws = torch.full((2 * need,), 0xFF, dtype=torch.uint8, device="cuda")
+    for nbytes, split in ((need - 4, False), (need, True), (2 * need, True)):
+        y = torch.empty((T, O), device="cuda")
+        st = _lib.call("sharq_linear_mxfp4", a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(),
+                       w.scales.data_ptr(), T, O, K, y.data_ptr(), O, 0, ws.data_ptr(), nbytes,
+                       torch.cuda.current_stream().cuda_stream)
+        assert st == _lib.SHARQ_OK
+        assert torch.equal(y, sq.linear_mxfp4(a, w, split_k=split))
+        assert (ws[need:] == 0xFF).all() and (split or (ws == 0xFF).all())

@@ -236,3 +236,13 @@ def test_refusals(sq):
             sq.moe_route(x, **bad)
     with pytest.raises(sq.SharqError):
         sq.moe_route(x[:1].expand(4, 12), 2)  # rows that overlap
+
+
+@pytest.mark.parametrize("T,E,groups,top,k", [(22, 128, 128, 40, 40), (41, 64, 64, 64, 64), (300, 128, 128, 64, 64),
+                                              (64, 16, 16, 16, 16)])
+def test_many_small_groups(sq, T, E, groups, top, k):
+    """The most LDS a token takes; token counts whose last wave is partly empty."""
+    print(f"small groups T={T} E={E} {top}/{groups} k={k}", flush=True)
+    rng = np.random.default_rng(T)
+    run(sq, rng.standard_normal((T, E)), k, groups=groups, top_groups=top, group_score="sum2", score="sigmoid",
+        bias=0.1 * rng.standard_normal(E).astype(np.float32))
