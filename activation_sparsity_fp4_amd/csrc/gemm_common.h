@@ -50,17 +50,19 @@ struct TileRows {
 
 // Weight rows of one output tile: the weight row behind tile column c.
 // Plain tiles take rows n0 + c. A fused gate|up tile over h columns
-// [h0, h0 + 128) of a weight whose rows are [gate (I rows); up (I rows)]
-// alternates 64-row blocks: block b = c / 64 holds the gate (b even) or up
-// (b odd) rows of h columns h0 + 64 (b / 2) + c % 64, so each wave's four
-// 32-column MFMA tiles are gate, gate, up, up of the same 64 h columns.
+// from h0 on, of a weight whose rows are [gate (I rows); up (I rows)],
+// alternates blocks of 2^shift rows: block b holds the gate (b even) or up
+// (b odd) rows of h columns h0 + 2^shift (b / 2) + c % 2^shift, so that half of
+// each wave's 32-column MFMA tiles (four with shift 6, two with 5) are gate and
+// half up columns of the same h columns.
 struct TileCols {
   int64_t n0;    // first output column (plain) or first h column (gate|up)
   int64_t half;  // 0 for a plain tile, else I
+  int shift = 6;
   __device__ __forceinline__ int64_t w_row(int c) const {
     if (half == 0) return n0 + c;
-    const int b = c >> 6;
-    return ((b & 1) ? half : 0) + n0 + 64 * (b >> 1) + (c & 63);
+    const int b = c >> shift;
+    return ((b & 1) ? half : 0) + n0 + ((int64_t)(b >> 1) << shift) + (c & ((1 << shift) - 1));
   }
 };
 

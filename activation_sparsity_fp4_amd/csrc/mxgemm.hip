@@ -49,12 +49,16 @@ struct MxTile {
   static constexpr int kRing = RING_;
   static constexpr int kWavesPerSimd = (WGS_ * kWaves + 3) / 4;
   static_assert(kRing >= 2 && WGS_ * kRing * kStage <= kLdsBytes, "ring");
-  static_assert(kRing * kStage >= kWaves * 32 * 272, "the epilogue's slabs fit in the ring's LDS");
-  static_assert(WN % 4 == 0 && BN == 256, "a wave holds gate, gate, up, up columns; one tile is 128 h columns");
 };
-using Mx32 = MxTile<1, 4, 1, 2, 3, 2>;
-using Mx64 = MxTile<2, 4, 1, 2, 3, 2>;
-using Mx128 = MxTile<2, 4, 2, 2, 3, 2>;
+// Large tiles load fewer operand bytes a MFMA; small ones are more, keep more
+// stages in flight and finish a stage sooner, which is what few tiles need.
+// (64 x 256 was between its neighbours everywhere; 32 x 128 and 32 x 64 gained
+// up to 7% for a few rows.)
+using Mx128x256 = MxTile<2, 4, 2, 2, 3, 2>;
+using Mx128x128 = MxTile<2, 2, 2, 2, 4, 2>;
+using Mx64x128 = MxTile<1, 2, 2, 2, 5, 2>;
+using Mx64x64 = MxTile<1, 1, 2, 2, 6, 2>;
+using Mx32x256 = MxTile<1, 4, 1, 2, 3, 2>;
 
 struct MxOperands {
   const uint8_t* a_codes;   // [G][rows][64]
@@ -90,14 +94,16 @@ struct MxScales {
 // by 8 (lane / 32), byte 0 (sub-step 0) and byte 2 (sub-step 1) are the blocks
 // of the lane's K half.
 template <class C, int SUB>
-constexpr int kScaleItems = SUB == 0 ? (C::WM + 1) / 2 + C::WN / 2 : 0;
+constexpr int kScaleItems = SUB == 0 ? (C::WM + 1) / 2 + (C::WN + 1) / 2 : 0;
 template <class C, int SUB>
 constexpr int kReadItems = kScaleItems<C, SUB> + C::WM + C::WN;
 
 // LDS reads of a slot: as many as finish the half's reads in the first 5/8 of
 // its slots, so that the other MFMAs cover the latency of the last ones.
 template <class C>
-constexpr int kReadsPerSlot = (kReadItems<C, 0> + C::kHalf * 5 / 8 - 1) / (C::kHalf * 5 / 8);
+constexpr int kReadSlots = C::kHalf * 5 / 8 < 1 ? 1 : C::kHalf * 5 / 8;
+template <class C>
+constexpr int kReadsPerSlot = (kReadItems<C, 0> + kReadSlots<C> - 1) / kReadSlots<C>;
 
 template <class C, int SUB, int R>
 __device__ __forceinline__ void mx_read(const uint8_t* st, MxFrags<C>& f, MxScales<C>& c, int wm, int wn, int lr,
@@ -111,7 +117,7 @@ __device__ __forceinline__ void mx_read(const uint8_t* st, MxFrags<C>& f, MxScal
     constexpr int j = 2 * (R - kSA);
     const uint8_t* p = st + C::kOffSW + 4 * (32 * C::WN * wn + 32 * j + lr);
     c.w[j] = *reinterpret_cast<const uint32_t*>(p);
-    c.w[j + 1] = *reinterpret_cast<const uint32_t*>(p + 128);
+    if constexpr (j + 1 < C::WN) c.w[j + 1] = *reinterpret_cast<const uint32_t*>(p + 128);
   } else if constexpr (R < kS + C::WM) {
     constexpr int i = R - kS;
     f.a[i] = frag(st + C::kOffA + swz(32 * C::WM * wm + 32 * i + lr, 2 * SUB + lh));
@@ -300,7 +306,7 @@ __device__ __forceinline__ void mx_loop(const MxOperands& op, const TileRows& tr
     if (src >= 0) ld.s_off = (uint32_t)(src * 4);
   } else if (!act_scales) {
     const int64_t o = tc.w_row(4 * lane);  // four rows of one 64-row block
-    if (o < op.O) ld.s_off = (uint32_t)(o * 4);
+    if (4 * lane < C::BN && o < op.O) ld.s_off = (uint32_t)(o * 4);
   } else if (4 * lane < C::BM && tr.m0 + 4 * lane < op.rows) {
     ld.s_off = (uint32_t)((tr.m0 + 4 * lane) * 4);
   }
@@ -368,18 +374,21 @@ __device__ __forceinline__ void mx_zero(v16f (&acc)[C::WM][C::WN]) {
 // Epilogues
 // ---------------------------------------------------------------------------
 
-constexpr int kSlabStride = 272;  // 256 bytes of a row + 16, so that rows start on distinct banks
-
 // Store the tile to y (fp32, or bf16 rounded to nearest even). A wave turns
-// slabs of 32 tokens x 256 bytes (64 fp32 or 128 bf16 columns) through LDS of
-// its own, so that every global store is 16 bytes a lane in 256-byte row runs.
+// slabs of 32 tokens x 256 bytes (64 fp32 or 128 bf16 columns; fewer where the
+// wave has fewer) through LDS of its own, so that every global store is 16 bytes
+// a lane in row runs of that length.
 // wide: y rows are 16-byte aligned (leading dimension included).
 template <class C, class Out>
 __device__ __forceinline__ void mx_store(const v16f (&acc)[C::WM][C::WN], uint8_t* lds, Out* __restrict__ y,
                                          int64_t ldy, const TileRows& tr, int64_t n0, int64_t O, bool wide) {
   constexpr bool kBf16 = sizeof(Out) == 2;
-  constexpr int kJ = kBf16 ? 4 : 2;         // MFMA column tiles of a slab
-  constexpr int kPer = 16 / sizeof(Out);    // columns of a 16-byte piece
+  constexpr int kMost = kBf16 ? 4 : 2;
+  constexpr int kJ = C::WN < kMost ? C::WN : kMost;  // MFMA column tiles of a slab
+  constexpr int kPer = 16 / sizeof(Out);             // columns of a 16-byte piece
+  constexpr int kPieces = 32 * kJ / kPer;            // of a row
+  constexpr int kSlabStride = 16 * kPieces + 16;     // 16 more, so that rows start on distinct banks
+  static_assert(C::kRing * C::kStage >= C::kWaves * 32 * kSlabStride, "the slabs fit in the ring's LDS");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave % C::NWM, wn = wave / C::NWM;
   const int lr = lane & 31, lh = lane >> 5;
@@ -406,8 +415,8 @@ __device__ __forceinline__ void mx_store(const v16f (&acc)[C::WM][C::WN], uint8_
           }
         }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = 4 * q + (lane >> 4), piece = lane & 15;
+      for (int q = 0; q < kPieces / 2; ++q) {
+        const int r = 64 / kPieces * q + lane / kPieces, piece = lane % kPieces;
         const uint4 v = *reinterpret_cast<const uint4*>(slab + r * kSlabStride + 16 * piece);
         const int64_t o = n0 + 32 * (C::WN * wn + j0) + kPer * piece;
         if (row0 + r < tr.rows_valid) {
@@ -460,42 +469,54 @@ __device__ __forceinline__ v2u half_swap(uint32_t x, uint32_t y) {
   return __builtin_amdgcn_permlane32_swap(x, y, false, false);
 }
 
-// h = bf16(silu(gate) * up) of the tile, coded to MXFP4: a wave's four MFMA
-// column tiles are gate, gate, up, up of 64 h columns, i.e. two blocks of each
-// of its tokens. Lane l holds half of both blocks of token l % 32; after the
-// half-wave swap it holds all of block l / 32 and writes its 16 bytes.
+// h columns of a gate|up tile, and the row blocks that alternate in its weight rows.
+template <class C>
+constexpr int kHCols = C::BN / 2;
+template <class C>
+constexpr int kHShift = C::WN == 4 ? 6 : 5;
+
+// h = bf16(silu(gate) * up) of the tile, coded to MXFP4: the first half of a
+// wave's MFMA column tiles is gate, the second up, of one block of its tokens
+// each. Lane l holds half of a block of token l % 32. Two blocks are coded
+// together (two of a token, or with one a token those of two row tiles): after
+// the half-wave swap lane l holds all of block l / 32 and writes its 16 bytes.
 template <class C>
 __device__ __forceinline__ void mx_silu_store(const v16f (&acc)[C::WM][C::WN], const TileRows& tr, int64_t h0,
                                               const MxH& out) {
-  static_assert(C::WN == 4, "gate, gate, up, up");
+  static_assert(C::WN == 4 || C::WN == 2, "gate, gate, up, up or gate, up");
+  constexpr int kJ = C::WN / 2;                        // blocks of a token in this wave
+  constexpr int kRows = kJ == 2 || C::WM == 1 ? 1 : 2;  // row tiles coded together
+  static_assert(C::WM % kRows == 0, "row tiles in pairs");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave % C::NWM, wn = wave / C::NWM;
   const int lr = lane & 31, lh = lane >> 5;
-  const int64_t block = (h0 >> 5) + 2 * wn + lh;  // the block this lane writes
+  const int64_t block = (h0 >> 5) + kJ * wn + (kJ == 2 ? lh : 0);  // the block this lane writes
   const int64_t blocks = out.I >> 5, padded = (blocks + 3) & ~(int64_t)3;
+  const bool writes = kJ * kRows == 2 || lh == 0;
 #pragma unroll
-  for (int i = 0; i < C::WM; ++i) {
-    const int row = 32 * C::WM * wm + 32 * i + lr;
-    uint32_t code[2][2], amax[2], byte[2];
+  for (int i = 0; i < C::WM; i += kRows) {
+    const int row = 32 * C::WM * wm + 32 * (kRows == 2 ? i + lh : i) + lr;
+    uint32_t code[2][2], byte[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int q = 0; q < kJ * kRows; ++q) {
+      const v16f &gate = acc[kRows == 2 ? i + q : i][kRows == 2 ? 0 : q],
+                 &up = acc[kRows == 2 ? i + q : i][kJ + (kRows == 2 ? 0 : q)];
       float h[16], m = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
-        const uint32_t b = bf16x2_rne(silu_times(acc[i][j][r], acc[i][j + 2][r]),
-                                      silu_times(acc[i][j][r + 1], acc[i][j + 2][r + 1]));
+        const uint32_t b = bf16x2_rne(silu_times(gate[r], up[r]), silu_times(gate[r + 1], up[r + 1]));
         h[r] = bf16_lo(b);
         h[r + 1] = bf16_hi(b);
         m = fmaxf(m, fmaxf(fabsf(h[r]), fabsf(h[r + 1])));
       }
       const v2u both = half_swap(__float_as_uint(m), __float_as_uint(m));
-      amax[j] = max(both[0], both[1]);  // non-negative floats order as their bits
-      byte[j] = e8m0_from_amax_bits(amax[j]);
-      quantize16(h, scale_from_e8m0(byte[j]), code[j]);
+      byte[q] = e8m0_from_amax_bits(max(both[0], both[1]));  // non-negative floats order as their bits
+      quantize16(h, scale_from_e8m0(byte[q]), code[q]);
     }
+    if constexpr (kJ * kRows == 1) code[1][0] = code[0][0], code[1][1] = code[0][1], byte[1] = byte[0];
     const v2u lo = half_swap(code[0][0], code[1][0]);  // [0]: columns 0-3, 8-11; [1]: columns 4-7, 12-15
     const v2u hi = half_swap(code[0][1], code[1][1]);  // the same from column 16 on
-    if (row < tr.rows_valid && block < padded) {
+    if (writes && row < tr.rows_valid && block < padded) {
       const int64_t t = tr.m0 + row;
       const bool real = block < blocks;
       const uint4 c = make_uint4((lo[0] & 0xFFFFu) | (lo[1] << 16), (lo[0] >> 16) | (lo[1] & 0xFFFF0000u),
@@ -543,10 +564,10 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_linear_silu_
   SHARQ_MX_LDS(C)
   const TileIndex ti = tile_index(blockIdx.x, tiles_m, tiles_total);
   const TileRows tr = dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM);
-  const int64_t h0 = (int64_t)ti.tn * 128;
+  const int64_t h0 = (int64_t)ti.tn * kHCols<C>;
   v16f acc[C::WM][C::WN];
   mx_zero<C>(acc);
-  mx_mainloop<C, false>(op, tr, TileCols{h0, out.I}, lds, acc, 0, op.nsteps);
+  mx_mainloop<C, false>(op, tr, TileCols{h0, out.I, kHShift<C>}, lds, acc, 0, op.nsteps);
   mx_silu_store<C>(acc, tr, h0, out);
 }
 
@@ -657,10 +678,10 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_grouped_silu
   const GroupedTile g = grouped_tile<C, true>(seg, E, out.T, a_rows, op.rows, tiles_n);
   if (g.e < 0) return;
   mx_select_expert(op, g.e);
-  const int64_t h0 = (int64_t)g.col * 128;
+  const int64_t h0 = (int64_t)g.col * kHCols<C>;
   v16f acc[C::WM][C::WN];
   mx_zero<C>(acc);
-  mx_mainloop<C, true>(op, g.tr, TileCols{h0, out.I}, lds, acc, 0, op.nsteps);
+  mx_mainloop<C, true>(op, g.tr, TileCols{h0, out.I, kHShift<C>}, lds, acc, 0, op.nsteps);
   mx_silu_store<C>(acc, g.tr, h0, out);
 }
 
@@ -672,41 +693,134 @@ MxOperands mx_operands(const MxProduct& p) {
   return MxOperands{p.a_codes, p.a_scales, p.w_codes, p.w_scales, p.rows, p.O, (int)((p.K + 127) / 128)};
 }
 
-// Row tile of a dense product: 0 Mx32, 1 Mx64, 2 Mx128.
-int mx_row_tile(int64_t T) { return T <= 32 ? 0 : T <= 64 ? 1 : 2; }
-int64_t mx_tile_rows(int tile) { return tile == 0 ? 32 : tile == 1 ? 64 : 128; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Times of the K loop in microseconds a stage, for the choice of tiles alone:
+// of a workgroup on a CU of its own, and of each of several.
+struct MxTileCost {
+  int64_t rows, cols;
+  double alone, each;
+};
+constexpr int kMxTiles = 5;
+constexpr MxTileCost kTiles[kMxTiles] = {
+    {128, 256, 0.48, 0.47}, {128, 128, 0.22, 0.29}, {64, 128, 0.175, 0.205}, {64, 64, 0.135, 0.15}, {32, 256, 0.40, 0.30}};
+constexpr int kMx64x64 = 3;  // too narrow for gate and up columns in one wave
+
+// Calls f with the tile type of kTiles[tile].
+template <class F>
+void mx_with_tile(int tile, F f) {
+  switch (tile) {
+    case 0: f(Mx128x256{}); break;
+    case 1: f(Mx128x128{}); break;
+    case 2: f(Mx64x128{}); break;
+    case kMx64x64: f(Mx64x64{}); break;
+    default: f(Mx32x256{}); break;
+  }
+}
+
+// The K loops of a launch: `share` workgroups on the busiest CU, and no less
+// than the operands' bytes at the rate of memory.
+double mx_loop_cost(int tile, double share, int64_t steps, double operand_bytes) {
+  const MxTileCost& c = kTiles[tile];
+  const double each = c.each * share;
+  const double loop = (double)steps * (c.alone > each ? c.alone : each), stream = operand_bytes / 5.8e6;
+  return loop > stream ? loop + 0.1 * stream : stream + 0.1 * loop;
+}
+
+double mx_operand_bytes(double rows, double K) { return rows * K * 17.0 / 32.0; }
 
 struct MxPlan {
   int tile, S;
   int tiles_m, tiles_total;
 };
 
-// Split-K plan: the S in [1, 16] (each split over at least 4 stages, the
-// partials at most 256 MB) with the smallest of a cost fitted, for the choice
-// alone, to timed launches (S = 1 .. 16) of nine layer shapes from 512 x 8192
-// to 57344 x 8192 (O x K), T = 1 .. 1024: the K loop of a workgroup times the
-// workgroups of a CU, no less than the operands' streaming, and for S > 1 the
-// second launch and the partials' traffic. The pick is within 7% of the best S
-// on all of them: the Llama-3.1-70B down projection (8192 x 28672) at T = 1 92
-// us whole, 25 us with S = 6; 57344 x 8192 40 us whole, 45 us with S = 2.
+// Tile and K split of a dense product: the cheapest of all tiles and S in [1,
+// 16] (each split over at least 4 stages, the partials at most 256 MB) by the
+// loops above and, for S > 1, a second launch and the partials' traffic. The
+// constants are fitted to timed launches of all of them on 11 layer shapes from
+// 2048 x 768 to 57344 x 8192 (O x K), T = 1 .. 1024, whose best they pick but
+// for 1% on average and 13% at most. With 256 columns a tile alone the best was
+// 27% slower on average: 4096 x 4096 at T = 128 15.9 us, 64 x 64 tiles 8.9;
+// 4096 x 14336 at T = 1024 49.9 us, 128 x 128 tiles 37.9; 28672 x 4096 at T = 1
+// 16.3 us, 64 x 128 tiles 12.8; and the other way round 57344 x 8192 at T = 1
+// 42 us, 45 to 50 with narrower tiles, 28672 x 4096 at T = 1024 72 us, 128 x 128
+// tiles 81. Split: 8192 x 28672 at T = 1 47 us whole, 24 us with S = 3.
 MxPlan mx_plan(int64_t T, int64_t O, int64_t K, bool may_split) {
-  MxPlan p{mx_row_tile(T), 1, 0, 0};
-  const int64_t bm = mx_tile_rows(p.tile);
-  p.tiles_m = (int)((T + bm - 1) / bm);
-  p.tiles_total = p.tiles_m * (int)((O + 255) / 256);
-  if (!may_split) return p;
-  const int64_t nsteps = (K + 127) / 128;
-  const int64_t s_max = nsteps / 4 < kMxMaxSplits ? nsteps / 4 : kMxMaxSplits;
-  const double stage = p.tile == 0 ? 0.65 : p.tile == 1 ? 0.67 : 0.79;
-  const double stream = ((double)O * (double)K + (double)T * (double)K) * 17.0 / 32.0 / 4.8e6;
+  const int64_t nsteps = ceil_div(K, 128);
+  const int64_t s_max = !may_split || nsteps < 8 ? 1 : nsteps / 4 < kMxMaxSplits ? nsteps / 4 : kMxMaxSplits;
+  const double bytes = mx_operand_bytes((double)O + (double)T, (double)K), out = (double)T * (double)O * 4.0;
+  MxPlan p{0, 1, 0, 0};
   double best = 0;
-  for (int64_t s = 1; s <= s_max && (s == 1 || s * T * O * 4 <= ((int64_t)256 << 20)); ++s) {
-    const double loop = (double)((nsteps + s - 1) / s) * stage * (double)((s * p.tiles_total + 255) / 256);
-    double t = loop > stream ? loop : stream;
-    if (s > 1) t += 6.2 + (double)(2 * s + 1) * (double)T * (double)O * 4.0 / 1.37e6;
-    if (s == 1 || t < best) best = t, p.S = (int)s;
+  for (int t = 0; t < kMxTiles; ++t) {
+    const int64_t tiles = ceil_div(T, kTiles[t].rows) * ceil_div(O, kTiles[t].cols);
+    for (int64_t s = 1; s <= s_max && (s == 1 || s * T * O * 4 <= ((int64_t)256 << 20)); ++s) {
+      if (s * tiles >= kMxMaxWorkgroups) break;
+      double us = mx_loop_cost(t, (double)ceil_div(s * tiles, 256), ceil_div(nsteps, s), bytes);
+      if (s > 1) us += 2.5 + 0.1 * (double)s + (double)(2 * s + 1) * out / 4.7e6;
+      if ((t == 0 && s == 1) || us < best) best = us, p.tile = t, p.S = (int)s;
+    }
   }
+  p.tiles_m = (int)ceil_div(T, kTiles[p.tile].rows);
+  p.tiles_total = p.tiles_m * (int)ceil_div(O, kTiles[p.tile].cols);
   return p;
+}
+
+// Column tiles of a gate|up product: they cover whole stages of h, 128 columns.
+int64_t mx_silu_cols(int64_t I, int tile) { return ceil_div(I, 128) * (256 / kTiles[tile].cols); }
+
+// Tile of a gate|up product whose K is not split, by the same costs: 2 x 14336 x
+// 4096 at T = 1 19 us with 128 x 256, 13 with 64 x 128; 2 x 28672 x 8192 at T = 8
+// 43 us with 32 x 256, 47 with the others; 2 x 4096 x 2048 at T = 512 12.6 us
+// with 128 x 256, 9.9 with 128 x 128.
+MxPlan mx_silu_plan(int64_t T, int64_t I, int64_t K) {
+  MxPlan p{0, 1, 0, 0};
+  double best = 0;
+  for (int t = 0; t < kMxTiles; ++t) {
+    const int64_t tiles = ceil_div(T, kTiles[t].rows) * mx_silu_cols(I, t);
+    if (t == kMx64x64 || (t > 0 && tiles >= kMxMaxWorkgroups)) continue;
+    const double us = mx_loop_cost(t, (double)ceil_div(tiles, 256), ceil_div(K, 128),
+                                   mx_operand_bytes(2.0 * (double)I + (double)T, (double)K));
+    if (t == 0 || us < best) best = us, p.tile = t;
+  }
+  p.tiles_m = (int)ceil_div(T, kTiles[p.tile].rows);
+  p.tiles_total = p.tiles_m * (int)mx_silu_cols(I, p.tile);
+  return p;
+}
+
+// Row slots of a grouped launch: no sorted segments of P rows fill more tiles.
+int64_t mx_row_slots(int64_t P, int64_t E, int tile) {
+  const int64_t filled = P < E ? P : E;
+  return filled + (P - filled) / kTiles[tile].rows;
+}
+
+// Tile of a grouped product of `cols` columns (or h columns) of O weight rows,
+// by the same costs for segments of about P / E rows, half a row tile more each
+// for what does not fill one, and 1 us for every 512 workgroups' lookup of their
+// tile. Fitted to timed launches of 18 expert layers (8 to 128 experts, 8 to
+// 32768 pairs; within 1% of the best on average, 7% at most): the gate|up of 4096
+// tokens x 8 of 128 experts (2048 -> 2 x 768) 93 us with 128 x 256, 117 and
+// more with the others; of 4 tokens 14.4 us with 64 x 128, 16.1 with 128 x 256;
+// the down product of 500 tokens x 3 of 16 experts (1024 -> 2080) 13.5 us with
+// 128 x 256, 11.2 with 128 x 128.
+int mx_grouped_tile(int64_t P, int64_t E, int64_t O, int64_t K, bool silu) {
+  const double filled = (double)(P < E ? P : E), mean = (double)P / filled;
+  const double bytes = mx_operand_bytes(filled * (double)O + (double)P, (double)K);
+  int pick = 0;
+  double best = 0;
+  for (int t = 0; t < kMxTiles; ++t) {
+    const int64_t cols = silu ? mx_silu_cols(O / 2, t) : ceil_div(O, kTiles[t].cols);
+    if ((silu && t == kMx64x64) || (t > 0 && mx_row_slots(P, E, t) * cols + 8 > kMxMaxWorkgroups)) continue;
+    const double rows = mean / (double)kTiles[t].rows + 0.5;
+    const double tiles = filled * (rows > 1 ? rows : 1) * (double)cols;
+    const double us = mx_loop_cost(t, tiles > 256 ? tiles / 256 : 1, ceil_div(K, 128), bytes) + ceil(tiles / 512);
+    if (t == 0 || us < best) best = us, pick = t;
+  }
+  return pick;
+}
+
+// A multiple of 8, of which the XCDs take equal shares.
+dim3 mx_grouped_grid(int64_t P, int64_t E, int tile, int64_t cols) {
+  return dim3((unsigned)((mx_row_slots(P, E, tile) * cols + 7) / 8 * 8));
 }
 
 bool mx_wide(const void* y, int64_t ldy, int64_t bytes) {
@@ -716,44 +830,45 @@ bool mx_wide(const void* y, int64_t ldy, int64_t bytes) {
 template <class Out>
 void launch_mx_store(const MxPlan& p, const MxOperands& op, Out* y, int64_t ldy, hipStream_t stream) {
   const bool wide = mx_wide(y, ldy, sizeof(Out));
-#define SHARQ_MX(C)                                                                                               \
-  hipLaunchKernelGGL((mx_linear_kernel<C, Out>), dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, y, ldy,  \
-                     wide, p.tiles_m, p.tiles_total)
-  if (p.tile == 0) SHARQ_MX(Mx32);
-  else if (p.tile == 1) SHARQ_MX(Mx64);
-  else SHARQ_MX(Mx128);
-#undef SHARQ_MX
+  mx_with_tile(p.tile, [&](auto c) {
+    using C = decltype(c);
+    hipLaunchKernelGGL((mx_linear_kernel<C, Out>), dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, y, ldy, wide,
+                       p.tiles_m, p.tiles_total);
+  });
 }
 
 void launch_mx_split(const MxPlan& p, const MxOperands& op, float* partials, hipStream_t stream) {
   const bool wide = op.O % 4 == 0;
-#define SHARQ_MX(C)                                                                                              \
-  hipLaunchKernelGGL(mx_split_kernel<C>, dim3(p.tiles_total* p.S), dim3(C::kThreads), 0, stream, op, p.tiles_m, \
-                     p.tiles_total, p.S, wide, partials)
-  if (p.tile == 0) SHARQ_MX(Mx32);
-  else if (p.tile == 1) SHARQ_MX(Mx64);
-  else SHARQ_MX(Mx128);
-#undef SHARQ_MX
+  mx_with_tile(p.tile, [&](auto c) {
+    using C = decltype(c);
+    hipLaunchKernelGGL(mx_split_kernel<C>, dim3(p.tiles_total * p.S), dim3(C::kThreads), 0, stream, op, p.tiles_m,
+                       p.tiles_total, p.S, wide, partials);
+  });
 }
 
-// Row tile of a grouped product, from the mean rows of an expert.
-int mx_grouped_tile(int64_t P, int32_t E) { return P <= 16 * (int64_t)E ? 0 : P <= 64 * (int64_t)E ? 1 : 2; }
+}  // namespace
+
+namespace {
+
+int64_t mx_workspace(const MxPlan& p, int64_t T, int64_t O) { return p.S > 1 ? (int64_t)p.S * T * O * 4 : 0; }
+
+// The plan of a product with a workspace of so many bytes.
+MxPlan mx_plan_with(const MxProduct& m, const void* workspace, int64_t workspace_bytes) {
+  const MxPlan p = mx_plan(m.rows, m.O, m.K, workspace != nullptr);
+  return mx_workspace(p, m.rows, m.O) <= workspace_bytes ? p : mx_plan(m.rows, m.O, m.K, false);
+}
 
 }  // namespace
 
 int64_t mx_linear_workspace_bytes(int64_t T, int64_t O, int64_t K) {
-  if (T <= 0 || O <= 0) return 0;
-  const MxPlan p = mx_plan(T, O, K, true);
-  return p.S > 1 ? (int64_t)p.S * T * O * 4 : 0;
+  return T <= 0 || O <= 0 ? 0 : mx_workspace(mx_plan(T, O, K, true), T, O);
 }
 
 hipError_t launch_mx_linear(const MxProduct& m, void* y, int64_t ldy, bool bf16, void* workspace,
                             int64_t workspace_bytes, hipStream_t stream) {
   const MxOperands op = mx_operands(m);
-  const int64_t need = mx_linear_workspace_bytes(m.rows, m.O, m.K);
-  const bool split = need > 0 && workspace && workspace_bytes >= need;
-  const MxPlan p = mx_plan(m.rows, m.O, m.K, split);
-  if (!split) {
+  const MxPlan p = mx_plan_with(m, workspace, workspace_bytes);
+  if (p.S == 1) {
     if (bf16) launch_mx_store(p, op, static_cast<uint16_t*>(y), ldy, stream);
     else launch_mx_store(p, op, static_cast<float*>(y), ldy, stream);
     return hipGetLastError();
@@ -776,10 +891,8 @@ hipError_t launch_mx_linear_silu(const MxProduct& m, uint8_t* h_codes, uint8_t* 
                                  int64_t workspace_bytes, hipStream_t stream) {
   const MxOperands op = mx_operands(m);
   const MxH out{h_codes, h_scales, m.rows, m.O / 2};
-  const int64_t need = mx_linear_workspace_bytes(m.rows, m.O, m.K);
-  const bool split = need > 0 && workspace && workspace_bytes >= need;
-  MxPlan p = mx_plan(m.rows, m.O, m.K, split);
-  if (split) {
+  MxPlan p = mx_plan_with(m, workspace, workspace_bytes);
+  if (p.S > 1) {
     float* partials = static_cast<float*>(workspace);
     launch_mx_split(p, op, partials, stream);
     const hipError_t e = hipGetLastError();
@@ -789,42 +902,36 @@ hipError_t launch_mx_linear_silu(const MxProduct& m, uint8_t* h_codes, uint8_t* 
                        out);
     return hipGetLastError();
   }
-  const int tiles_n = (int)((out.I + 127) / 128);
-  p.tiles_total = p.tiles_m * tiles_n;
-#define SHARQ_MX(C)                                                                                                 \
-  hipLaunchKernelGGL(mx_linear_silu_kernel<C>, dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, out, p.tiles_m, \
-                     p.tiles_total)
-  if (p.tile == 0) SHARQ_MX(Mx32);
-  else if (p.tile == 1) SHARQ_MX(Mx64);
-  else SHARQ_MX(Mx128);
-#undef SHARQ_MX
+  p = mx_silu_plan(m.rows, out.I, m.K);
+  mx_with_tile(p.tile, [&](auto c) {
+    using C = decltype(c);
+    if constexpr (C::WN > 1)
+      hipLaunchKernelGGL(mx_linear_silu_kernel<C>, dim3(p.tiles_total), dim3(C::kThreads), 0, stream, op, out,
+                         p.tiles_m, p.tiles_total);
+  });
   return hipGetLastError();
 }
 
-int64_t mx_grouped_workgroups(int64_t P, int32_t E, int64_t tiles_n) {
-  const int64_t bm = mx_tile_rows(mx_grouped_tile(P, E));
-  return ((P + bm - 1) / bm + E) * tiles_n;
+bool mx_grouped_fits(int64_t P, int32_t E, int64_t O) {
+  return mx_row_slots(P, E, 0) * ceil_div(O, 256) + 8 <= kMxMaxWorkgroups;
 }
 
 hipError_t launch_mx_grouped(const MxProduct& m, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
                              void* y, bool bf16, hipStream_t stream) {
   const MxOperands op = mx_operands(m);
-  const int tiles_n = (int)((m.O + 255) / 256), tile = mx_grouped_tile(P, E);
-  const dim3 grid((unsigned)mx_grouped_workgroups(P, E, tiles_n));
+  const int tile = mx_grouped_tile(P, E, m.O, m.K, false);
+  const int tiles_n = (int)ceil_div(m.O, kTiles[tile].cols);
+  const dim3 grid = mx_grouped_grid(P, E, tile, tiles_n);
   const bool wide = mx_wide(y, m.O, bf16 ? 2 : 4);
-#define SHARQ_MX(C)                                                                                                  \
-  do {                                                                                                               \
-    if (bf16)                                                                                                        \
-      hipLaunchKernelGGL((mx_grouped_kernel<C, uint16_t>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, \
-                         static_cast<uint16_t*>(y), P, wide, tiles_n);                                               \
-    else                                                                                                             \
-      hipLaunchKernelGGL((mx_grouped_kernel<C, float>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E,    \
-                         static_cast<float*>(y), P, wide, tiles_n);                                                  \
-  } while (0)
-  if (tile == 0) SHARQ_MX(Mx32);
-  else if (tile == 1) SHARQ_MX(Mx64);
-  else SHARQ_MX(Mx128);
-#undef SHARQ_MX
+  mx_with_tile(tile, [&](auto c) {
+    using C = decltype(c);
+    if (bf16)
+      hipLaunchKernelGGL((mx_grouped_kernel<C, uint16_t>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E,
+                         static_cast<uint16_t*>(y), P, wide, tiles_n);
+    else
+      hipLaunchKernelGGL((mx_grouped_kernel<C, float>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E,
+                         static_cast<float*>(y), P, wide, tiles_n);
+  });
   return hipGetLastError();
 }
 
@@ -832,15 +939,15 @@ hipError_t launch_mx_grouped_silu(const MxProduct& m, const int32_t* a_rows, con
                                   uint8_t* h_codes, uint8_t* h_scales, hipStream_t stream) {
   const MxOperands op = mx_operands(m);
   const MxH out{h_codes, h_scales, P, m.O / 2};
-  const int tiles_n = (int)((out.I + 127) / 128), tile = mx_grouped_tile(P, E);
-  const dim3 grid((unsigned)mx_grouped_workgroups(P, E, tiles_n));
-#define SHARQ_MX(C)                                                                                            \
-  hipLaunchKernelGGL(mx_grouped_silu_kernel<C>, grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, out, \
-                     tiles_n)
-  if (tile == 0) SHARQ_MX(Mx32);
-  else if (tile == 1) SHARQ_MX(Mx64);
-  else SHARQ_MX(Mx128);
-#undef SHARQ_MX
+  const int tile = mx_grouped_tile(P, E, m.O, m.K, true);
+  const int tiles_n = (int)mx_silu_cols(out.I, tile);
+  const dim3 grid = mx_grouped_grid(P, E, tile, tiles_n);
+  mx_with_tile(tile, [&](auto c) {
+    using C = decltype(c);
+    if constexpr (C::WN > 1)
+      hipLaunchKernelGGL(mx_grouped_silu_kernel<C>, grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, out,
+                         tiles_n);
+  });
   return hipGetLastError();
 }
 

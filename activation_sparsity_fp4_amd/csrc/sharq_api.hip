@@ -399,8 +399,8 @@ bool mx_aligned(const sharq::MxProduct& m) {
   return aligned16(m.a_codes) && aligned16(m.a_scales) && aligned16(m.w_codes) && aligned16(m.w_scales);
 }
 
-// Workgroups of a dense product's grid: one row tile up to 128 rows, 16 the largest K split.
-bool mx_grid_ok(int64_t T, int64_t O) { return ((T + 127) / 128) * ((O + 255) / 256) * 16 < kMaxGroupedTiles; }
+// Workgroups of a dense product's grid in its largest tile; 16 is the largest K split.
+bool mx_grid_ok(int64_t T, int64_t O) { return ((T + 127) / 128) * ((O + 255) / 256) * 16 < sharq::kMxMaxWorkgroups; }
 
 int check_workspace(const void* workspace, int64_t bytes) {
   if (bytes < 0 || (bytes > 0 && !workspace)) return SHARQ_EINVAL;
@@ -451,11 +451,11 @@ int sharq_linear_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, con
 namespace {
 
 int check_mx_grouped(const sharq::MxProduct& m, const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
-                     int64_t P, int64_t tiles_n) {
+                     int64_t P) {
   const int rc = check_mx(m.rows, m.O, m.K);
   if (rc != SHARQ_OK) return rc;
   if (E < 1 || P < 0 || P >= ((int64_t)1 << 31) || (!a_rows && m.rows < P)) return SHARQ_EINVAL;
-  if (sharq::mx_grouped_workgroups(P, E, tiles_n) >= kMaxGroupedTiles) return SHARQ_EINVAL;
+  if (!sharq::mx_grouped_fits(P, E, m.O)) return SHARQ_EINVAL;
   if (P == 0 || m.O == 0) return SHARQ_OK;
   if (mx_null(m) || !seg_offsets) return SHARQ_EINVAL;
   if (!mx_aligned(m) || ((uintptr_t)seg_offsets & 3u) || ((uintptr_t)a_rows & 3u)) return SHARQ_EALIGN;
@@ -469,7 +469,7 @@ int sharq_linear_grouped_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, 
                                int64_t P, int64_t O, int64_t K, void* y, int dtype, hipStream_t stream) {
   const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T_src, O, K};
   if (dtype != SHARQ_F32 && dtype != SHARQ_BF16) return SHARQ_EINVAL;
-  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P, (O + 255) / 256);
+  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P);
   if (rc != SHARQ_OK || P == 0 || O == 0) return rc;
   if (!y) return SHARQ_EINVAL;
   if (!aligned16(y)) return SHARQ_EALIGN;
@@ -482,7 +482,7 @@ int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_sca
                                     uint8_t* h_codes, uint8_t* h_scales, hipStream_t stream) {
   if (I <= 0 || I % 32 != 0 || I >= kMaxMxRows / 2 || P >= kMaxMxRows) return SHARQ_EINVAL;
   const sharq::MxProduct m{a_codes, a_scales, w_codes, w_scales, T_src, 2 * I, K};
-  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P, (I + 127) / 128);
+  const int rc = check_mx_grouped(m, a_rows, seg_offsets, E, P);
   if (rc != SHARQ_OK || P == 0) return rc;
   if (!h_codes || !h_scales) return SHARQ_EINVAL;
   if (!aligned16(h_codes) || !aligned16(h_scales)) return SHARQ_EALIGN;

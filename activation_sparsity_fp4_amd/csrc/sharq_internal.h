@@ -102,7 +102,8 @@ hipError_t launch_mx_linear(const MxProduct& m, void* y, int64_t ldy, bool bf16,
 // O = 2 I: gate rows, then up rows
 hipError_t launch_mx_linear_silu(const MxProduct& m, uint8_t* h_codes, uint8_t* h_scales, void* workspace,
                                  int64_t workspace_bytes, hipStream_t stream);
-int64_t mx_grouped_workgroups(int64_t P, int32_t E, int64_t tiles_n);
+constexpr int64_t kMxMaxWorkgroups = (int64_t)1 << 24;  // fewer than 2^32 threads
+bool mx_grouped_fits(int64_t P, int32_t E, int64_t O);  // O: weight rows of an expert
 hipError_t launch_mx_grouped(const MxProduct& m, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
                              void* y, bool bf16, hipStream_t stream);
 hipError_t launch_mx_grouped_silu(const MxProduct& m, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,

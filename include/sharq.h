@@ -561,9 +561,8 @@ SHARQ_API int sharq_linear_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_s
  *  y [P][O] of type dtype; h_codes u8 [ceil(I/128)][P][64], h_scales.
  * Malformed segment or gather contents are handled as sharq_linear_grouped
  * does. seg_offsets and a_rows need 4-byte alignment only. Requires T_src, O <
- * 2^25 (P < 2^25 for the fused form) and fewer than 2^24 workgroups:
- * (ceil(P / rows) + E) * ceil(O / 256), rows = 32 for P <= 16 E, 64 for P <=
- * 64 E, else 128 (O / 256: I / 128 for the fused form).
+ * 2^25 (P < 2^25 for the fused form) and (P / 128 + min(P, E)) * (O / 256 + 1)
+ * < 2^24 (workgroups).
  */
 SHARQ_API int sharq_linear_grouped_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t T_src,
                                const int32_t* a_rows, const int32_t* seg_offsets, int32_t E, const uint8_t* w_codes,

@@ -564,3 +564,85 @@ def test_workspace_too_small_is_no_split(sq):
         assert st == _lib.SHARQ_OK
         assert torch.equal(y, sq.linear_mxfp4(a, w, split_k=split))
         assert (ws[need:] == 0xFF).all() and (split or (ws == 0xFF).all())
+
+
+# Shapes for which the library takes its larger tiles (128 x 256, 128 x 128, 64 x 128, 32 x 256), whole and split.
+LARGE = [(70, 128, 33000), (70, 160, 16416), (1, 128, 16416), (3, 160, 33000), (4100, 96, 4200), (1030, 544, 2500),
+         (130, 28672, 4128), (70, 8224, 8200), (1, 8224, 4128), (2, 28672, 16416), (600, 14336, 4096)]
+
+
+@pytest.mark.parametrize("T,K,O", LARGE)
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+def test_linear_of_large_shapes(sq, T, K, O, out):
+    """Sampled rows and columns, the ends of tiles among them, against the oracle."""
+    import torch
+    print(f"large linear T={T} K={K} O={O} {out}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(T + O)
+    a, w = _random_mx(sq, gen, T, K=K), _random_mx(sq, gen, O, K=K)
+    rng = np.random.default_rng(T + K)
+
+    def pick(n):
+        edges = [0, 31, 32, 63, 64, 127, 128, 255, 256, n // 2, n - 65, n - 2, n - 1]
+        return np.unique([i for i in edges + list(rng.integers(0, n, 20)) if 0 <= i < n])
+
+    def sample(q, at):
+        i = torch.from_numpy(at).cuda()
+        rows = lambda x, n: to_np(x[:, i].permute(1, 0, 2).reshape(len(at), -1))[:, :n]  # noqa: E731
+        return rows(q.codes, K // 2), rows(q.scales, K // 32)
+
+    t, o = pick(T), pick(O)
+    ref, bound = linear_mxfp4_ref(*sample(a, t), *sample(w, o))
+    for split in (True, False):
+        y = sq.linear_mxfp4(a, w, dtype=torch.float32 if out == "fp32" else torch.bfloat16, split_k=split)
+        assert y.isfinite().all()
+        _close(y[torch.from_numpy(t).cuda()][:, torch.from_numpy(o).cuda()], ref, bound, K)
+
+
+@pytest.mark.parametrize("T,K,I", [(8, 8192, 28672), (64, 4096, 14336), (128, 4096, 14336), (300, 4096, 14336),
+                                   (515, 2048, 4128), (8200, 160, 288), (4100, 96, 256)])
+def test_silu_of_large_shapes_equals_the_chain(sq, T, K, I):
+    import torch
+    print(f"large silu T={T} K={K} I={I}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    a, w = _random_mx(sq, gen, T, K=K), _random_mx(sq, gen, 2 * I, K=K)
+    w.scales[w.scales > 0] -= 8  # gate and up of order 1 and 10
+    for split in (True, False):
+        h = sq.linear_silu_mxfp4(a, w, split_k=split)
+        want = sq.quantize_mxfp4(sq.silu_mul(sq.linear_mxfp4(a, w, split_k=split)))
+        assert torch.equal(h.scales, want.scales) and torch.equal(h.codes, want.codes)
+
+
+@pytest.mark.parametrize("T,E,P,K,I", [(90, 16, 700, 128, 2080), (500, 70, 4100, 160, 256), (3, 3, 3, 128, 4096),
+                                       (20, 70, 71, 160, 512), (64, 128, 512, 2048, 768), (1, 128, 8, 2048, 768),
+                                       (256, 8, 512, 1024, 4128), (1000, 128, 8000, 544, 768)])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+def test_grouped_of_large_shapes(sq, T, E, P, K, I, out):
+    """Every expert's rows equal those of a dense call of their own; the fused form equals its chain. Some experts
+    are empty, some rows behind the last segment."""
+    import torch
+    print(f"large grouped T={T} E={E} P={P} K={K} I={I} {out}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(E + P)
+    rng = np.random.default_rng(P)
+    share = rng.dirichlet(np.where(rng.random(E) < 0.2, 1e-3, 3.0))
+    seg = np.concatenate([[0], np.cumsum(rng.multinomial(P - min(3, P - 1), share))]).astype(np.int32)
+    rows = rng.integers(0, T, P).astype(np.int32)
+    a, w = _random_mx(sq, gen, T, K=K), _random_mx(sq, gen, E, 2 * I, K=K)
+    w.scales[w.scales > 0] -= 8
+    dtype = torch.float32 if out == "fp32" else torch.bfloat16
+    y = torch.full((P, 2 * I), 7.0, dtype=dtype, device="cuda")
+    sq.linear_grouped_mxfp4(a, w, i32_to_gpu(seg), i32_to_gpu(rows), out=y)
+    n = int(seg[-1])
+    for e in np.unique([int(np.argmax(np.diff(seg))), *np.flatnonzero(np.diff(seg))[[0, -1]]]):
+        at = torch.from_numpy(rows[seg[e]:seg[e + 1]]).long().cuda()
+        one = sq.linear_mxfp4(_rows_of(sq, a, at), sq.MXFP4(w.codes[e], w.scales[e], K), dtype=dtype, split_k=False)
+        assert torch.equal(y[seg[e]:seg[e + 1]], one), e
+    assert (y[n:] == 7).all()
+    ordered = _rows_of(sq, a, torch.from_numpy(rows).long().cuda())
+    plain = torch.full((P, 2 * I), 7.0, dtype=dtype, device="cuda")
+    sq.linear_grouped_mxfp4(ordered, w, i32_to_gpu(seg), out=plain)
+    assert torch.equal(plain, y)
+    if out == "fp32":
+        for act, gather in ((a, i32_to_gpu(rows)), (ordered, None)):
+            h = sq.linear_grouped_silu_mxfp4(act, w, i32_to_gpu(seg), gather)
+            want = sq.quantize_mxfp4(sq.silu_mul(y))
+            assert torch.equal(h.scales[:, :n], want.scales[:, :n]) and torch.equal(h.codes[:, :n], want.codes[:, :n])
