@@ -143,16 +143,6 @@ __device__ __forceinline__ TileIndex tile_index(int b, int tiles_m, int tiles_to
   return tile_order(xcd_item(b, tiles_total), tiles_m, tiles_total);
 }
 
-// Inclusive prefix sum across a 64-lane wave.
-__device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
-  return v;
-}
-
 // Tile of a grouped launch. The grid is one-dimensional over (row slot,
 // column tile) pairs, column tiles innermost. With kXcdRanges the pairs are
 // remapped so that each XCD (to which workgroups are dealt round-robin)
@@ -174,61 +164,76 @@ __device__ __forceinline__ int64_t seg_bound(const int32_t* __restrict__ seg, in
   return v < lo ? lo : v > P ? P : v;
 }
 
+// Row tiles of 64 experts, one a lane, and their prefix sums.
+struct ExpertTiles {
+  int64_t lo, hi;  // the expert's rows
+  int incl, excl;  // row tiles up to and before it
+};
 template <class C>
-__device__ __forceinline__ int expert_row_tiles(const int32_t* __restrict__ seg, int e, int E, int64_t P) {
-  if (e >= E) return 0;
-  const int64_t lo = seg_bound(seg, e, 0, P);
-  return (int)((seg_bound(seg, e + 1, lo, P) - lo + C::BM - 1) / C::BM);
+__device__ __forceinline__ ExpertTiles expert_tiles(const int32_t* __restrict__ seg, int e, int E, int64_t P) {
+  ExpertTiles t;
+  const int at = e < E ? e : E - 1;
+  t.lo = seg_bound(seg, at, 0, P);
+  t.hi = e < E ? seg_bound(seg, at + 1, t.lo, P) : t.lo;
+  const int tiles = (int)((t.hi - t.lo + C::BM - 1) / C::BM);
+  t.incl = wave_inclusive_scan(tiles);
+  t.excl = t.incl - tiles;
+  return t;
 }
 
 template <class C, bool kXcdRanges>
 __device__ __forceinline__ GroupedTile grouped_tile(const int32_t* __restrict__ seg, int E, int64_t P,
                                                     const int32_t* __restrict__ a_rows, int64_t src_rows,
                                                     int tiles_n) {
-  __shared__ int s_info[3];
+  __shared__ int64_t s_rows[2];
+  __shared__ int s_info[2];
   const int tid = threadIdx.x;
   if (tid == 0) s_info[0] = -1;
   __syncthreads();
   if (tid < 64) {
-    // With kXcdRanges, pass 1 counts the real tiles A; the first A (rounded
-    // up to 8) workgroups take the work, so that every XCD gets an equal
-    // share, XCD x the logical range [x A8 / 8, (x + 1) A8 / 8).
+    // Experts 0 .. 127 are read once, in one round trip to memory; later ones
+    // by the passes that need them.
+    constexpr int kHeld = 2;
+    ExpertTiles held[kHeld];
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) held[c] = expert_tiles<C>(seg, 64 * c + tid, E, P);
+    // With kXcdRanges, the real tiles A are counted; the first A (rounded up
+    // to 8) workgroups take the work, so that every XCD gets an equal share,
+    // XCD x the logical range [x A8 / 8, (x + 1) A8 / 8).
     const int b = blockIdx.x;
     int logical = b, target = b / tiles_n;  // slots past the last tile find no expert
     if constexpr (kXcdRanges) {
       int rows_total = 0;
-      for (int e0 = 0; e0 < E; e0 += 64) {
-        int tiles = expert_row_tiles<C>(seg, e0 + tid, E, P);
-        for (int off = 32; off > 0; off >>= 1) tiles += __shfl_xor(tiles, off, 64);
-        rows_total += tiles;
-      }
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) rows_total += __builtin_amdgcn_readlane(held[c].incl, 63);
+      for (int e0 = 64 * kHeld; e0 < E; e0 += 64)
+        rows_total += __builtin_amdgcn_readlane(expert_tiles<C>(seg, e0 + tid, E, P).incl, 63);
       const int A = rows_total * tiles_n, A8 = (A + 7) & ~7;
       logical = b < A8 ? (b & 7) * (A8 >> 3) + (b >> 3) : A;
       target = logical < A ? logical / tiles_n : -1;
     }
-    if (tid == 0) s_info[2] = logical - (logical / tiles_n) * tiles_n;
-    // Pass 2: the expert holding row slot target.
+    // The expert holding row slot target.
     int base = 0;
-    for (int e0 = 0; e0 < E && target >= 0; e0 += 64) {
-      const int e = e0 + tid;
-      const int tiles = expert_row_tiles<C>(seg, e, E, P);
-      const int incl = wave_inclusive_scan(tiles, tid);
-      const int excl = incl - tiles;
-      if (e < E && target >= base + excl && target < base + incl) {
+    auto find = [&](int e, const ExpertTiles& t) {
+      if (target >= base + t.excl && target < base + t.incl) {
         s_info[0] = e;
-        s_info[1] = target - base - excl;
+        s_info[1] = logical - (logical / tiles_n) * tiles_n;
+        s_rows[0] = t.lo + (int64_t)(target - base - t.excl) * C::BM;
+        s_rows[1] = t.hi;
       }
-      base += __shfl(incl, 63, 64);
-    }
+      base += __builtin_amdgcn_readlane(t.incl, 63);
+    };
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) find(64 * c + tid, held[c]);
+    for (int e0 = 64 * kHeld; e0 < E && target >= base; e0 += 64) find(e0 + tid, expert_tiles<C>(seg, e0 + tid, E, P));
   }
   __syncthreads();
   GroupedTile g;
   g.e = s_info[0];
-  g.col = s_info[2];
   if (g.e >= 0) {
-    const int64_t lo = seg_bound(seg, g.e, 0, P);
-    g.tr.m0 = lo + (int64_t)s_info[1] * C::BM;
-    const int64_t hi = seg_bound(seg, g.e + 1, lo, P);
+    g.col = s_info[1];
+    g.tr.m0 = s_rows[0];
+    const int64_t hi = s_rows[1];
     g.tr.rows_valid = hi - g.tr.m0 < C::BM ? hi - g.tr.m0 : C::BM;
     g.tr.gather = a_rows;
     g.tr.src_rows = src_rows;

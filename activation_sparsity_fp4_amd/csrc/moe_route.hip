@@ -144,17 +144,15 @@ __device__ void plan_chunk(const RouteArgs& a, int64_t t0, int64_t t1, int* tota
                            int chunk, int chunks) {
   __shared__ int wave_sum[16];
   const int tid = threadIdx.x, nthreads = blockDim.x;
+  // this thread's first expert id, on its way while the scan runs
+  const int first_id = tid < (t1 - t0 < 64 ? t1 - t0 : 64) * a.k ? a.expert[t0 * a.k + tid] : -1;
+  auto id_of = [&](int64_t s0, int p) { return s0 == t0 && p == tid ? first_id : a.expert[s0 * a.k + p]; };
   // exclusive scan of totals over the experts, nthreads at a time
   int carry = 0;
   for (int e0 = 0; e0 < a.E; e0 += nthreads) {
     const int e = e0 + tid;
     const int v = e < a.E ? totals[e] : 0;
-    int incl = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(incl, d, 64);
-      if ((tid & 63) >= d) incl += u;
-    }
+    const int incl = wave_inclusive_scan(v);
     if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
     __syncthreads();
     int sum = carry;
@@ -180,12 +178,12 @@ __device__ void plan_chunk(const RouteArgs& a, int64_t t0, int64_t t1, int* tota
     for (int e = tid; e < a.E; e += nthreads) bits[e] = 0;
     __syncthreads();
     for (int p = tid; p < pairs; p += nthreads) {
-      const int e = a.expert[s0 * a.k + p];
+      const int e = id_of(s0, p);
       if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&bits[e]), 1ull << token_of(p));
     }
     __syncthreads();
     for (int p = tid; p < pairs; p += nthreads) {
-      const int e = a.expert[s0 * a.k + p], t = token_of(p);
+      const int e = id_of(s0, p), t = token_of(p);
       int at = -1;
       if (e >= 0) {
         at = before[e] + __popcll(bits[e] & ((1ull << t) - 1));
@@ -505,7 +503,7 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs a, int64_t chu
   if (part < parts)
     for (int e = tid - part * width; e < a.E; e += width) {
       int sum = 0, pre = 0;
-#pragma unroll 16
+#pragma unroll 32
       for (int r = part; r < chunks; r += parts) {
         const int v = a.counts[(int64_t)r * a.E + e];
         sum += v;

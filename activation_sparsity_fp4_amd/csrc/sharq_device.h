@@ -102,4 +102,16 @@ __device__ __forceinline__ uint32_t amax_bits32(const float (&v)[32]) {
   return __float_as_uint(m);
 }
 
+// Inclusive prefix sum across a 64-lane wave: within the rows of 16 lanes, then
+// each odd row takes its left neighbour's last lane, then the upper half lane 31.
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 }  // namespace sharq

@@ -646,3 +646,27 @@ def test_grouped_of_large_shapes(sq, T, E, P, K, I, out):
             h = sq.linear_grouped_silu_mxfp4(act, w, i32_to_gpu(seg), gather)
             want = sq.quantize_mxfp4(sq.silu_mul(y))
             assert torch.equal(h.scales[:, :n], want.scales[:, :n]) and torch.equal(h.codes[:, :n], want.codes[:, :n])
+
+
+@pytest.mark.parametrize("E,P", [(127, 300), (128, 300), (129, 300), (300, 900), (1000, 70)])
+def test_grouped_over_many_experts(sq, E, P):
+    """More experts than a workgroup holds of the segments at once; tiles of every one of them."""
+    import torch
+    print(f"many experts E={E} P={P}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    rng = np.random.default_rng(E)
+    K, I, T = 96, 64, 40
+    seg = np.concatenate([[0], np.cumsum(rng.multinomial(P - 2, np.full(E, 1 / E)))]).astype(np.int32)
+    rows = rng.integers(0, T, P).astype(np.int32)
+    a, w = _random_mx(sq, gen, T, K=K), _random_mx(sq, gen, E, 2 * I, K=K)
+    y = torch.full((P, 2 * I), 7.0, device="cuda")
+    sq.linear_grouped_mxfp4(a, w, i32_to_gpu(seg), i32_to_gpu(rows), out=y)
+    for e in np.flatnonzero(np.diff(seg)):
+        at = torch.from_numpy(rows[seg[e]:seg[e + 1]]).long().cuda()
+        one = sq.linear_mxfp4(_rows_of(sq, a, at), sq.MXFP4(w.codes[e], w.scales[e], K), split_k=False)
+        assert torch.equal(y[seg[e]:seg[e + 1]], one), e
+    n = int(seg[-1])
+    assert (y[n:] == 7).all()
+    h = sq.linear_grouped_silu_mxfp4(a, w, i32_to_gpu(seg), i32_to_gpu(rows))
+    want = sq.quantize_mxfp4(sq.silu_mul(y))
+    assert torch.equal(h.scales[:, :n], want.scales[:, :n]) and torch.equal(h.codes[:, :n], want.codes[:, :n])
