@@ -16,6 +16,7 @@ The plain MXFP4 path (one operand, no decomposition) and expert routing:
 
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 from . import _lib
@@ -775,6 +776,12 @@ def _out_dtype(out, dtype):
     return dtype, 0 if dtype == torch.float32 else 1
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name, *shape):
+    """The library's answer for a shape (asking it takes a fifth of a small call)."""
+    return _lib.call(name, *shape)
+
+
 def _scratch(device, nbytes):
     """Workspace of one call, from the allocator that orders it with the
     stream's work (in a graph, from the graph's own memory); None for 0."""
@@ -801,7 +808,7 @@ def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True)
         _check_matrix(out, dtype, T, O, "out")
         ldy = out.stride(0) if T > 1 else O
     _same_device(a.codes, a.scales, w.codes, w.scales, out)
-    ws = _scratch(dev, _lib.call("sharq_linear_mxfp4_workspace_bytes", T, O, K) if split_k else 0)
+    ws = _scratch(dev, _workspace_bytes("sharq_linear_mxfp4_workspace_bytes", T, O, K) if split_k else 0)
     _run("sharq_linear_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
          T, O, K, out.data_ptr(), ldy, number, _ptr(ws), 0 if ws is None else ws.numel())
     return out
@@ -832,7 +839,7 @@ def linear_silu_mxfp4(a: MXFP4, w_gu: MXFP4, out: Optional[MXFP4] = None, split_
         if out.K != I or out.codes.shape[1] != T:
             raise ValueError(f"out must be an MXFP4 tensor of [{T}, {I}]")
     _same_device(a.codes, a.scales, w_gu.codes, w_gu.scales, out.codes, out.scales)
-    ws = _scratch(dev, _lib.call("sharq_linear_silu_mxfp4_workspace_bytes", T, I, K) if split_k else 0)
+    ws = _scratch(dev, _workspace_bytes("sharq_linear_silu_mxfp4_workspace_bytes", T, I, K) if split_k else 0)
     _run("sharq_linear_silu_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w_gu.codes.data_ptr(),
          w_gu.scales.data_ptr(), T, I, K, out.codes.data_ptr(), out.scales.data_ptr(), _ptr(ws),
          0 if ws is None else ws.numel())
@@ -960,7 +967,7 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     a_rows, expert, pair_index, weight = torch.empty((4, T, k), dtype=torch.int32, device=dev).unbind(0)
     r = Routing(expert, weight.view(torch.float32), torch.empty(E + 1, dtype=torch.int32, device=dev),
                 a_rows.view(-1), pair_index)
-    ws = _scratch(dev, _lib.call("sharq_moe_route_workspace_bytes", T, E)) if T > 1 else None
+    ws = _scratch(dev, _workspace_bytes("sharq_moe_route_workspace_bytes", T, E)) if T > 1 else None
     _run("sharq_moe_route", dev, logits.data_ptr(), kind, T, E, logits.stride(0) if T > 1 else E, _ptr(bias), k,
          _SCORES[score], groups, groups if top_groups is None else top_groups, _GROUP_SCORES[group_score],
          int(renormalize), float(scale), _ptr(num_tokens), expert.data_ptr(), weight.data_ptr(),
