@@ -392,8 +392,8 @@ constexpr int kRouteThreads = NE <= 8 ? 1024 : 512;
 // the experts, then k slots of every token in flight, then, with groups,
 // group_doubles of every token in flight. Bound by the chain of a token (load,
 // k rounds of a maximum over its lanes, float64 weights) at few tokens, by the
-// vector instructions of its rounds at many: 1 x 128, k = 8: 6.7 us; 4096 x
-// 128 bf16: 6.9 us; 16384 x 256 with bias and 4 of 8 groups: 35 us (16.8 MB
+// vector instructions of its rounds at many: 1 x 128, k = 8: 6.3 us; 4096 x
+// 128 bf16: 7.1 us; 16384 x 256 with bias and 4 of 8 groups: 35 us (16.8 MB
 // read, 2.1 MB written: 4 us at the rate of a copy).
 template <int LANES, int NE, bool kBias>
 __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
 
 // Places of chunk blockIdx.x from the counts of all chunks: every workgroup
 // reads the whole table (at most 256 rows, in L2) rather than wait for a scan
-// of it in a launch between. 4096 x 128, k = 8: 7.4 us; 16384 x 256: 9.8 us.
+// of it in a launch between. 4096 x 128, k = 8: 6.9 us; 16384 x 256: 9.2 us.
 __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   uint64_t* bits = reinterpret_cast<uint64_t*>(lds);
