@@ -250,8 +250,8 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
                 raise ValueError(f"gamma must hold K = {K} entries, got {gamma.numel()}")
             gamma = gamma.contiguous()
         _same_device(x, gamma, out.codes, out.scales)
-        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, x.stride(0), _ptr(gamma), float(rms_eps), 0,
-             out.codes.data_ptr(), out.scales.data_ptr())
+        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, x.stride(0) if R > 1 else K, _ptr(gamma),
+             float(rms_eps), 0, out.codes.data_ptr(), out.scales.data_ptr())
         return out
     st = _lib.call("sharq_quantize_mxfp4", x.data_ptr(), R, K, x.stride(0), out.codes.data_ptr(),
                    out.scales.data_ptr(), _stream(x.device))

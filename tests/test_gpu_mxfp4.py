@@ -670,3 +670,25 @@ def test_grouped_over_many_experts(sq, E, P):
     h = sq.linear_grouped_silu_mxfp4(a, w, i32_to_gpu(seg), i32_to_gpu(rows))
     want = sq.quantize_mxfp4(sq.silu_mul(y))
     assert torch.equal(h.scales[:, :n], want.scales[:, :n]) and torch.equal(h.codes[:, :n], want.codes[:, :n])
+
+
+def test_one_row_of_any_stride(sq):
+    """A single row has no leading dimension: whatever stride its tensor reports, and rows of a wider tensor."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(1, 320, device="cuda", generator=gen, dtype=torch.bfloat16)
+    column = x.reshape(320, 1).t()
+    assert column.shape == (1, 320) and column.stride(0) != 320
+    want = sq.quantize_mxfp4(x, rms_eps=1e-5)
+    got = sq.quantize_mxfp4(column, rms_eps=1e-5)
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    w = _random_mx(sq, gen, 40, K=320)
+    y = torch.full((40, 3), 7.0, device="cuda").t()[:1]  # one row, unit column stride refused
+    with pytest.raises(ValueError):
+        sq.linear_mxfp4(want, w, out=y)
+    y = torch.zeros((1, 40), device="cuda").expand(1, 40)
+    sq.linear_mxfp4(want, w, out=y)
+    assert torch.equal(y, sq.linear_mxfp4(want, w))
+    logits = torch.randn(24, 1, device="cuda", generator=gen).t()
+    r, s = sq.moe_route(logits, 3), sq.moe_route(logits.contiguous(), 3)
+    assert all(torch.equal(a, b) for a, b in zip(r, s))
