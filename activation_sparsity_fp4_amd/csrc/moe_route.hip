@@ -7,8 +7,7 @@
 // first taken in float32 with a bound on their error; only where two of the
 // values that decide (a round's largest and the next, two groups) lie within
 // the bound is the wave's selection done again in float64, so the choice is
-// float64's at about a third of its time (16384 x 256 with groups: 50 us with
-// every score in float64). A token's experts lie in LANES lanes, NE
+// float64's at about a third of its time. A token's experts lie in LANES lanes, NE
 // neighbouring ones in each, so of equal values the lowest lane and the lowest
 // register hold the lowest expert. A round takes the largest value as an
 // unsigned integer of the same order (0: cannot be chosen): a register
@@ -204,8 +203,14 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Doubles of LDS that the groups of a token take: its values, the groups' scores and which are kept.
-__host__ __device__ constexpr int group_doubles(int E, int groups) { return E + groups + (groups + 1) / 2; }
+// Doubles of LDS that the groups of a token take: its values (a.group_values of
+// them), the groups' scores and which are kept. A group that is a power of two of
+// whole lanes needs no values: its score is found by lane exchanges. (With the
+// values always, 16384 x 256 with 8 groups had room for 16 tokens in flight
+// instead of 32: 42 us, 35 so.)
+__host__ __device__ inline int group_doubles(const RouteArgs& a) {
+  return a.group_values + a.groups + (a.groups + 1) / 2;
+}
 
 template <class V>
 __device__ __forceinline__ void take_two(V v, V& first, V& second) {
@@ -222,10 +227,10 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, const V (&v)[NE]
                                             V near) {
   const int size = a.E / a.groups;
   V* buf = reinterpret_cast<V*>(lds);
-  V* gscore = buf + a.E;
-  int* kept = reinterpret_cast<int*>(lds + a.E + a.groups);
-  const int lanes = size / NE;  // lanes of a group, where a lane's experts belong to one
-  if (size % NE == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LANES) {
+  V* gscore = buf + a.group_values;
+  int* kept = reinterpret_cast<int*>(lds + a.group_values + a.groups);
+  if (a.group_values == 0) {
+    const int lanes = size / NE;
     // the two largest of each lane, then of the aligned lanes of a group
     V first = kNegInf, second = kNegInf;
 #pragma unroll
@@ -393,7 +398,7 @@ constexpr int kRouteThreads = NE <= 8 ? 1024 : 512;
 // group_doubles of every token in flight. Bound by the chain of a token (load,
 // k rounds of a maximum over its lanes, float64 weights) at few tokens, by the
 // vector instructions of its rounds at many: 1 x 128, k = 8: 6.3 us; 4096 x
-// 128 bf16: 7.1 us; 16384 x 256 with bias and 4 of 8 groups: 35 us (16.8 MB
+// 128 bf16: 7.0 us; 16384 x 256 with bias and 4 of 8 groups: 29 us (16.8 MB
 // read, 2.1 MB written: 4 us at the rate of a copy).
 template <int LANES, int NE, bool kBias>
 __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
@@ -407,7 +412,7 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
   int* before = counts + a.E;
   int* chosen = before + a.E + (int64_t)slot * a.k;
   double* gbuf = reinterpret_cast<double*>(before + a.E + ((int64_t)flight * a.k + 1) / 2 * 2) +
-                 (int64_t)slot * group_doubles(a.E, a.groups);
+                 (int64_t)slot * group_doubles(a);
   for (int e = tid; e < a.E; e += blockDim.x) counts[e] = 0, before[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * chunk_tokens;
@@ -488,7 +493,7 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
 
 // Places of chunk blockIdx.x from the counts of all chunks: every workgroup
 // reads the whole table (at most 256 rows, in L2) rather than wait for a scan
-// of it in a launch between. 4096 x 128, k = 8: 6.9 us; 16384 x 256: 9.2 us.
+// of it in a launch between. 4096 x 128, k = 8: 6.2 us; 16384 x 256: 7.8 us.
 __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   uint64_t* bits = reinterpret_cast<uint64_t*>(lds);
@@ -503,11 +508,23 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs a, int64_t chu
   if (part < parts)
     for (int e = tid - part * width; e < a.E; e += width) {
       int sum = 0, pre = 0;
-#pragma unroll 32
-      for (int r = part; r < chunks; r += parts) {
-        const int v = a.counts[(int64_t)r * a.E + e];
-        sum += v;
-        pre += r < c ? v : 0;
+      // rows on their way together: 32, then 4 at a time (the last row again behind the end)
+      const int32_t* at = a.counts + (part * a.E + e);
+      const int step = parts * a.E;
+      int r = part;
+      for (; r + 31 * parts < chunks; r += 32 * parts, at += 32 * step) {
+        int v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = at[i * step];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum += v[i], pre += r + i * parts < c ? v[i] : 0;
+      }
+      for (; r < chunks; r += 4 * parts, at += 4 * step) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = r + i * parts < chunks ? at[i * step] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += v[i], pre += r + i * parts < c ? v[i] : 0;
       }
       atomicAdd(&totals[e], sum);
       atomicAdd(&before[e], pre);
@@ -526,9 +543,11 @@ int64_t chunk_tokens(int64_t T) {
 }
 
 template <int LANES, int NE>
-void launch_route(const RouteArgs& a, int64_t per, int chunks, hipStream_t stream) {
+void launch_route(RouteArgs a, int64_t per, int chunks, hipStream_t stream) {
+  const int size = a.E / a.groups, lanes = size / NE;
+  a.group_values = size % NE == 0 && (lanes & (lanes - 1)) == 0 ? 0 : a.E;
   // tokens in flight: the chunk's, at most a workgroup's worth and 64 KB of LDS, in whole waves
-  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a.E, a.groups) : 0);
+  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a) : 0);
   const int64_t fixed = 16 * (int64_t)a.E + 8;  // 8: the groups' doubles are aligned
   constexpr int64_t kWaveTokens = 64 / LANES;
   int64_t waves = ((a.T < per ? a.T : per) + kWaveTokens - 1) / kWaveTokens;

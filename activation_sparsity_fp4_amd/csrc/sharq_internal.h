@@ -128,6 +128,7 @@ struct RouteArgs {
   float* weight;
   int32_t *seg_offsets, *a_rows, *pair_index;
   int32_t* counts;  // workspace: [chunks][E]
+  int32_t group_values = 0;  // set by the launch
 };
 int64_t moe_route_workspace_bytes(int64_t T, int32_t E);
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
