@@ -6,8 +6,9 @@
 // scores are monotone in it), score + bias in float64 with one. Scores are
 // first taken in float32 with a bound on their error; only where two of the
 // values that decide (a round's largest and the next, two groups) lie within
-// the bound is the wave's selection done again in float64, so the choice is
-// float64's at about a third of its time. A token's experts lie in LANES lanes, NE
+// the bound is the order of the chosen found by their float64 values, or, where
+// even the set is open, the wave's selection done again in float64, so the choice
+// is float64's at about a third of its time. A token's experts lie in LANES lanes, NE
 // neighbouring ones in each, so of equal values the lowest lane and the lowest
 // register hold the lowest expert. A round takes the largest value as an
 // unsigned integer of the same order (0: cannot be chosen): a register
@@ -220,8 +221,8 @@ __device__ __forceinline__ void take_two(V v, V& first, V& second) {
 
 // Clears the keys of experts outside the token's top_groups groups. v: what
 // the groups compare, -inf for an expert that cannot be chosen; buf: the
-// token's group_doubles in LDS. True where two groups' scores are at most
-// `near` apart (never for near < 0).
+// token's group_doubles in LDS. True where scores at most `near` apart leave open
+// whether a group stays (never for near < 0).
 template <int LANES, int NE, class V, class Key>
 __device__ __forceinline__ bool keep_groups(const RouteArgs& a, const V (&v)[NE], Key (&key)[NE], int lt, double* lds,
                                             V near) {
@@ -257,14 +258,16 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, const V (&v)[NE]
   bool close = false;
   for (int g = lt; g < a.groups; g += LANES) {
     const V mine = gscore[g];
-    int rank = 0;
+    int rank = 0, above = 0, not_below = -1;  // -1: the group itself is not below
 #pragma unroll 4
     for (int o = 0; o < a.groups; ++o) {
       const V other = gscore[o];
       rank += other > mine || (other == mine && o < g);
-      close |= o != g && fabs(other - mine) <= near;
+      above += other > mine + near;
+      not_below += other >= mine - near;
     }
     kept[g] = rank < a.top_groups;
+    close |= near >= 0 && mine > (V)kNegInf && above < a.top_groups && not_below >= a.top_groups;
   }
   wave_sync();
   int g = lt * NE / size, in = lt * NE - g * size;
@@ -282,9 +285,14 @@ __device__ __forceinline__ float score_exp(float x) { return __expf(x); }
 __device__ __forceinline__ double score_inverse(double x) { return 1.0 / x; }
 __device__ __forceinline__ float score_inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 
+// What a selection by float32 values leaves to do.
+enum : int { kTold, kOrder, kAgain };
+
 // The k best experts of a wave's tokens, x their logits (-inf: cannot be
-// chosen), into chosen[j] (an expert or -1). True where values of type V
-// did not tell (a uniform answer; V = double always does).
+// chosen), into chosen[j] (an expert or -1). Where values of type V do not tell
+// (V = double always does), the answer, the same for the wave, is kOrder if the
+// first k + 1 (chosen[k] the first left out) are told from all others and only
+// their order is open, else kAgain.
 //
 // Error of the float32 scores, u = 2^-24: exp(y), y a rounded difference, is
 // off by at most (2.5 |y| + 2) u of it (the argument's two roundings, log2(e)'s
@@ -297,7 +305,7 @@ __device__ __forceinline__ float score_inverse(float x) { return __builtin_amdgc
 // follow each other in the order (the first left out among them) and are
 // closer than twice all that are taken for close.
 template <int LANES, int NE, bool kBias, class V>
-__device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE], int lane, int* chosen,
+__device__ __forceinline__ int select(const RouteArgs& a, const float (&x)[NE], int lane, int* chosen,
                                        double* gbuf) {
   using Key = typename std::conditional<sizeof(V) == 8, uint64_t, uint32_t>::type;
   constexpr bool kRough = kBias && sizeof(V) == 4;
@@ -306,7 +314,7 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
   Key key[NE];
   V value[NE];
   V bound = 0;
-  bool close = false;
+  bool again = false, order = false, last_close = false;
   const bool scores = kBias || (a.groups > 1 && a.sum2);
   if (scores) {
     V ref = 0, inv = 1;
@@ -348,16 +356,16 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
       most = token_reduce<LANES>(most, [](V p, V q) { return p > q ? p : q; });
       near = 4 * bound + most * (V)5e-7;
     }
-    close = keep_groups<LANES, NE, V, Key>(a, value, key, lt, gbuf, near);
+    again = keep_groups<LANES, NE, V, Key>(a, value, key, lt, gbuf, near);
   }
-  for (int j = lt; j < a.k; j += LANES) chosen[j] = -1;
+  for (int j = lt; j < a.k + (kBias ? 1 : 0); j += LANES) chosen[j] = -1;
   wave_sync();
   // the lanes of this lane's token below it, in a half of a ballot
   const uint32_t shift = lane & 31 & ~(LANES - 1);
   const uint32_t below = ((1u << (lt & 31)) - 1u) << shift;
   auto lanes_of = [&](uint64_t m) { return lane < 32 ? (uint32_t)m : (uint32_t)(m >> 32); };
   float last = 0.0f;
-  for (int j = 0; j < a.k + (kRough ? 1 : 0); ++j) {
+  for (int j = 0; j < a.k + (kRough ? 2 : 0); ++j) {
     Key head = key[0];
 #pragma unroll
     for (int i = 1; i < NE; ++i) head = max(head, key[i]);
@@ -365,9 +373,14 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
     if constexpr (kRough) {  // the one before, and this one: far enough apart to tell? (NaN, of infinities, is not)
       const float v = __uint_as_float((uint32_t)(best >> 31 ? best ^ 0x80000000u : ~best));
       const float rounding = (float)(NE + 1) * 1.2e-7f * fmaxf(fabsf(v), fabsf(last));
-      close |= j > 0 && best != 0 && !(last - v > 2.0f * ((float)bound + rounding));
+      const bool close = j > 0 && best != 0 && !(last - v > 2.0f * ((float)bound + rounding));
+      if (j == a.k + 1) {  // the last chosen, the first and the second left out: all close?
+        again |= last_close && close;
+        break;
+      }
+      order |= close;
+      last_close = close;
       last = v;
-      if (j == a.k) break;
     }
     const bool has = head == best && best != 0;
     const uint64_t have = __ballot(has);
@@ -385,7 +398,31 @@ __device__ __forceinline__ bool select(const RouteArgs& a, const float (&x)[NE],
     for (int i = 0; i < NE; ++i) key[i] = at == i ? 0 : key[i];
   }
   wave_sync();
-  return __any(close);
+  return __any(again) ? kAgain : __any(order) ? kOrder : kTold;
+}
+
+// chosen[0 .. k] into the order of float64's sigmoid + bias, a lane a slot (k <
+// LANES). Lanes of tokens whose order was told find it again. One such wave in a
+// launch is common (a pair of 4096 tokens' first nine of 128 is close in most of
+// them) and decides its time: with the whole selection again instead, 4096 x 128
+// with a bias 17.2 us, 15.3 so, with 4 of 8 groups 19.0 and 16.3.
+template <int LANES>
+__device__ __forceinline__ void order_chosen(const RouteArgs& a, int64_t t, int lane, int* chosen) {
+  const int lt = lane % LANES;
+  const int e = lt <= a.k ? chosen[lt] : -1;
+  double v = kNegInf;
+  if (e >= 0)
+    v = sigmoid64((double)fminf(load_logit(a.logits, a.dtype, t * a.ld + e), 3.4028234663852886e38f)) +
+        (double)a.bias[e];
+  int rank = 0;
+  for (int i = 0; i <= a.k; ++i) {
+    const double other = __shfl(v, i, LANES);
+    const int id = __shfl(e, i, LANES);
+    rank += id >= 0 && (other > v || (other == v && id < e));
+  }
+  wave_sync();
+  if (e >= 0 && rank < a.k) chosen[rank] = e;
+  wave_sync();
 }
 
 // Threads of a routing workgroup: 1024 (128 registers a lane), 512 where a lane
@@ -394,7 +431,7 @@ template <int NE>
 constexpr int kRouteThreads = NE <= 8 ? 1024 : 512;
 
 // Routes the tokens of chunk blockIdx.x. LDS: bit masks, counts and places of
-// the experts, then k slots of every token in flight, then, with groups,
+// the experts, then k slots (with a bias k + 1) of every token in flight, then, with groups,
 // group_doubles of every token in flight. Bound by the chain of a token (load,
 // k rounds of a maximum over its lanes, float64 weights) at few tokens, by the
 // vector instructions of its rounds at many: 1 x 128, k = 8: 6.3 us; 4096 x
@@ -410,8 +447,9 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
   uint64_t* bits = reinterpret_cast<uint64_t*>(lds);
   int* counts = reinterpret_cast<int*>(bits + a.E);
   int* before = counts + a.E;
-  int* chosen = before + a.E + (int64_t)slot * a.k;
-  double* gbuf = reinterpret_cast<double*>(before + a.E + ((int64_t)flight * a.k + 1) / 2 * 2) +
+  const int slots = a.k + (kBias ? 1 : 0);
+  int* chosen = before + a.E + (int64_t)slot * slots;
+  double* gbuf = reinterpret_cast<double*>(before + a.E + ((int64_t)flight * slots + 1) / 2 * 2) +
                  (int64_t)slot * group_doubles(a);
   for (int e = tid; e < a.E; e += blockDim.x) counts[e] = 0, before[e] = 0;
   __syncthreads();
@@ -429,8 +467,9 @@ __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs 
     if (a.dtype == 0) load_row<NE>(static_cast<const float*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
     else if (a.dtype == 1) load_row<NE>(static_cast<const uint16_t*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
     else load_row<NE>(static_cast<const _Float16*>(a.logits) + at_row, lt * NE, a.E, row, wide, x);
-    if (select<LANES, NE, kBias, float>(a, x, lane, chosen, gbuf))
-      select<LANES, NE, kBias, double>(a, x, lane, chosen, gbuf);
+    const int left = select<LANES, NE, kBias, float>(a, x, lane, chosen, gbuf);
+    if (kBias && left == kOrder && !softmax && a.k < LANES) order_chosen<LANES>(a, t, lane, chosen);
+    else if (left != kTold) select<LANES, NE, kBias, double>(a, x, lane, chosen, gbuf);
     double ref = 0.0, total = 1.0;  // softmax: the row's largest logit, and the sum of exp(x - ref)
     if (softmax && !a.renormalize) {
       float top = x[0];
@@ -547,7 +586,7 @@ void launch_route(RouteArgs a, int64_t per, int chunks, hipStream_t stream) {
   const int size = a.E / a.groups, lanes = size / NE;
   a.group_values = size % NE == 0 && (lanes & (lanes - 1)) == 0 ? 0 : a.E;
   // tokens in flight: the chunk's, at most a workgroup's worth and 64 KB of LDS, in whole waves
-  const int64_t token_bytes = 4 * a.k + (a.groups > 1 ? 8 * group_doubles(a) : 0);
+  const int64_t token_bytes = 4 * (a.k + (a.bias ? 1 : 0)) + (a.groups > 1 ? 8 * group_doubles(a) : 0);
   const int64_t fixed = 16 * (int64_t)a.E + 8;  // 8: the groups' doubles are aligned
   constexpr int64_t kWaveTokens = 64 / LANES;
   int64_t waves = ((a.T < per ? a.T : per) + kWaveTokens - 1) / kWaveTokens;

@@ -246,3 +246,30 @@ def test_many_small_groups(sq, T, E, groups, top, k):
     rng = np.random.default_rng(T)
     run(sq, rng.standard_normal((T, E)), k, groups=groups, top_groups=top, group_score="sum2", score="sigmoid",
         bias=0.1 * rng.standard_normal(E).astype(np.float32))
+
+
+@pytest.mark.parametrize("T,E,k,groups,top", [(200, 32, 5, 1, 1), (300, 128, 8, 1, 1), (300, 128, 15, 1, 1),
+                                              (200, 256, 8, 8, 4), (100, 512, 20, 16, 5), (40, 1000, 9, 1, 1),
+                                              (100, 64, 40, 1, 1), (50, 16, 16, 1, 1), (300, 60, 4, 12, 3)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gscore", ["max", "sum2"])
+def test_values_closer_than_float32_tells(sq, T, E, k, groups, top, score, gscore):
+    """Clusters of one to four logits a last place apart, so that the order inside the first k, the last place and
+    the kept groups hang on float64's scores, alone and together."""
+    print(f"close values T={T} E={E} k={k} {top}/{groups} {score} {gscore}", flush=True)
+    rng = np.random.default_rng(E + k)
+    x = np.empty((T, E), np.float32)
+    for t in range(T):
+        heads = rng.permutation(E).astype(np.float32) * np.float32(4.0 / E) - np.float32(1.0)
+        row, at = [], 0
+        while len(row) < E:
+            v = heads[at]
+            for _ in range(rng.integers(1, 5) if rng.random() < 0.3 else 1):
+                row.append(v)
+                v = np.nextafter(v, np.float32(9.0)) if rng.random() < 0.8 else v
+            at += 1
+        x[t] = rng.permutation(np.array(row[:E], np.float32))
+    bias = np.zeros(E, np.float32)
+    run(sq, x, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=gscore)
+    bias[rng.random(E) < 0.5] = 0.25
+    run(sq, x, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=gscore, renormalize=False)
