@@ -119,10 +119,10 @@ def _need(t, dtype, name, ndim=None):
 
 
 def _same_device(first, *others):
-    device = first.device
+    index = first.get_device()  # -1 off the GPU; cheaper than a torch.device
     for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
 
 
 def _run(name, device, *args):
@@ -746,15 +746,16 @@ def unpack_stage_major(codes, scales, K: int):
 
 
 def _check_mx(t, name, ndim=3):
-    """An MXFP4 tensor's codes and scales are contiguous, stage-major and fit its K."""
+    """The shape of an MXFP4 tensor's codes; codes and scales are contiguous, stage-major and fit its K."""
     torch = _torch()
-    codes, scales, G = t.codes, t.scales, stages(t.K)
+    codes, scales, K = t
+    G = stages(K)
     if type(codes) is type(scales) is torch.Tensor:
-        shape, sshape = codes.shape, scales.shape
-        if (codes.dtype is scales.dtype is torch.uint8 and codes.is_cuda and scales.is_cuda and len(shape) == ndim
-                and shape[-3] == G and shape[-1] == 64 and sshape[:-1] == shape[:-1] and sshape[-1] == 4
+        shape = codes.shape
+        if (len(shape) == ndim and shape[-3] == G and shape[-1] == 64 and scales.shape == (*shape[:-1], 4)
+                and codes.dtype is scales.dtype is torch.uint8 and codes.is_cuda and scales.is_cuda
                 and codes.is_contiguous() and scales.is_contiguous()):
-            return
+            return shape
     _need(codes, torch.uint8, name + ".codes", ndim)
     _need(scales, torch.uint8, name + ".scales", ndim)
     shape, sshape = codes.shape, scales.shape
@@ -763,6 +764,7 @@ def _check_mx(t, name, ndim=3):
                          f"got {tuple(shape)} and {tuple(sshape)}")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous")
+    return shape
 
 
 def _out_dtype(out, dtype):
@@ -795,11 +797,9 @@ def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True)
     split over a workspace where the library expects that to be faster (single
     tokens, few output tiles); the result is deterministic either way."""
     torch = _torch()
-    _check_mx(a, "a")
-    _check_mx(w, "w")
-    if w.K != a.K:
+    T, O, K = _check_mx(a, "a")[1], _check_mx(w, "w")[1], a.K
+    if w.K != K:
         raise ValueError("weight K does not match the activation K")
-    T, O, K = a.codes.shape[1], w.codes.shape[1], a.K
     dtype, number = _out_dtype(out, dtype)
     dev = a.codes.device
     if out is None:
@@ -826,11 +826,10 @@ def linear_silu_mxfp4(a: MXFP4, w_gu: MXFP4, out: Optional[MXFP4] = None, split_
     linear_mxfp4(split_k) -> silu_mul -> quantize_mxfp4 bit for bit; neither
     the product nor h passes through memory (but for the fp32 partials of a
     split K)."""
-    _check_mx(a, "a")
-    _check_mx(w_gu, "w_gu")
-    if w_gu.K != a.K or w_gu.codes.shape[1] % 2:
+    T, O, K = _check_mx(a, "a")[1], _check_mx(w_gu, "w_gu")[1], a.K
+    if w_gu.K != K or O % 2:
         raise ValueError("w_gu must be [2I, K] with the activation's K")
-    T, I, K = a.codes.shape[1], w_gu.codes.shape[1] // 2, a.K
+    I = O // 2
     dev = a.codes.device
     if out is None:
         out = _mx_like(T, I, dev)
@@ -849,11 +848,10 @@ def linear_silu_mxfp4(a: MXFP4, w_gu: MXFP4, out: Optional[MXFP4] = None, split_
 def _check_grouped(a, w, seg_offsets, a_rows, name):
     """(T_src, E, rows of the weight, P) of a grouped call on the plain path."""
     torch = _torch()
-    _check_mx(a, "a")
-    _check_mx(w, name, 4)
+    T = _check_mx(a, "a")[1]
+    E, _, O, _ = _check_mx(w, name, 4)
     if w.K != a.K:
         raise ValueError("weight K does not match the activation K")
-    E = w.codes.shape[0]
     _need(seg_offsets, torch.int32, "seg_offsets", 1)
     if seg_offsets.numel() != E + 1 or not seg_offsets.is_contiguous():
         raise ValueError("seg_offsets must be a contiguous [E + 1] tensor")
@@ -862,8 +860,7 @@ def _check_grouped(a, w, seg_offsets, a_rows, name):
         if not a_rows.is_contiguous():
             raise ValueError("a_rows must be contiguous")
     _same_device(a.codes, a.scales, w.codes, w.scales, seg_offsets, a_rows)
-    T = a.codes.shape[1]
-    return T, E, w.codes.shape[2], T if a_rows is None else a_rows.numel()
+    return T, E, O, T if a_rows is None else a_rows.numel()
 
 
 def linear_grouped_mxfp4(a: MXFP4, w: MXFP4, seg_offsets, a_rows=None, out=None, dtype=None):
@@ -941,10 +938,11 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     torch = _torch()
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
-    kind = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(logits.dtype)
+    dtype = logits.dtype
+    kind = 0 if dtype == torch.float32 else 1 if dtype == torch.bfloat16 else 2 if dtype == torch.float16 else None
     if kind is None:
-        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
-    _need(logits, logits.dtype, "logits", 2)
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {dtype}")
+    _need(logits, dtype, "logits", 2)
     T, E = logits.shape
     if T and (logits.stride(1) != 1 and E > 1):
         raise ValueError("logits rows must be contiguous along the experts")
