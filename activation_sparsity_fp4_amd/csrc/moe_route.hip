@@ -302,7 +302,7 @@ enum : int { kTold, kOrder, kAgain };
 // (2.5 ln 1024 + 2) u: p (2.5 |y| + 2 + 21 + 20 + 3) u < 3.5e-6 / sum, as p <=
 // 1 / sum and p |y| < 0.37 / sum. Adding the bias rounds by u of the result.
 // A key drops log2(NE) bits for the number of its register. Two values that
-// follow each other in the order (the first left out among them) and are
+// follow each other in the order (the first two left out among them) and are
 // closer than twice all that are taken for close.
 template <int LANES, int NE, bool kBias, class V>
 __device__ __forceinline__ int select(const RouteArgs& a, const float (&x)[NE], int lane, int* chosen,
