@@ -1118,8 +1118,7 @@ hipError_t launch_linear_grouped_silu_prepare(const uint8_t* bb_codes, const uin
   const HOutputs out{h, h_bb_codes, h_bb_scales, h_res_codes, h_res_scales, h_mask, P, I};
   const int64_t tiles_m_bound = (P + SmallTile::BM - 1) / SmallTile::BM + E;
   const int tiles_n = (int)(I / 128);
-  const int total = (int)(tiles_n * tiles_m_bound);
-  const dim3 grid((unsigned)total);
+  const dim3 grid((unsigned)((tiles_n * tiles_m_bound + 7) / 8 * 8));  // whole XCD ranges (grouped_tile)
   if (n == 2 && m == 4)
     hipLaunchKernelGGL((linear_grouped_silu_prepare_kernel<2, 4>), grid, dim3(kThreads), 0, stream, op, a_rows,
                        seg_offsets, E, w_codes, w_scales, out, tiles_n);

@@ -148,7 +148,9 @@ __device__ __forceinline__ TileIndex tile_index(int b, int tiles_m, int tiles_to
 // remapped so that each XCD (to which workgroups are dealt round-robin)
 // receives a contiguous range: the column tiles of one row tile then share
 // its activation rows, and the row tiles of one expert its weight tiles, in
-// that XCD's L2. Without it, pair b runs on XCD b mod 8, which for 8 column
+// that XCD's L2. The A real tiles are dealt over the first A rounded up to 8
+// workgroups, so the grid must be a multiple of 8 (a smaller one leaves tiles
+// to no workgroup). Without it, pair b runs on XCD b mod 8, which for 8 column
 // tiles gives each XCD a fixed column slice of every weight. The row slot is
 // a linear index over all (expert, row-tile) pairs, expert e holding
 // ceil(count_e / BM) row tiles in expert order; the expert is found by a wave-wide prefix sum of the
