@@ -355,8 +355,9 @@ __device__ __forceinline__ int select(const RouteArgs& a, const float (&x)[NE], 
       for (int i = 0; i < NE; ++i) most = value[i] > (V)kNegInf ? max(most, (V)fabs(value[i])) : most;
       most = token_reduce<LANES>(most, [](V p, V q) { return p > q ? p : q; });
       near = 4 * bound + most * (V)5e-7;
+      again = !(most < (V)8.5e37);  // below 2^126, so that no sum of two, nor a score + near, passes float32's range
     }
-    again = keep_groups<LANES, NE, V, Key>(a, value, key, lt, gbuf, near);
+    again |= keep_groups<LANES, NE, V, Key>(a, value, key, lt, gbuf, near);
   }
   for (int j = lt; j < a.k + (kBias ? 1 : 0); j += LANES) chosen[j] = -1;
   wave_sync();
