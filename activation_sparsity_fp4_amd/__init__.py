@@ -237,6 +237,7 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
     if x.stride(1) != 1:
         raise ValueError("x rows must be contiguous along K")
     R, K = x.shape
+    ldx = x.stride(0) if R > 1 else K
     if out is None:
         out = MXFP4(torch.empty((stages(K), R, 64), dtype=torch.uint8, device=x.device),
                     torch.empty((stages(K), R, 4), dtype=torch.uint8, device=x.device), K)
@@ -250,10 +251,10 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
                 raise ValueError(f"gamma must hold K = {K} entries, got {gamma.numel()}")
             gamma = gamma.contiguous()
         _same_device(x, gamma, out.codes, out.scales)
-        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, x.stride(0) if R > 1 else K, _ptr(gamma),
+        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, ldx, _ptr(gamma),
              float(rms_eps), 0, out.codes.data_ptr(), out.scales.data_ptr())
         return out
-    st = _lib.call("sharq_quantize_mxfp4", x.data_ptr(), R, K, x.stride(0), out.codes.data_ptr(),
+    st = _lib.call("sharq_quantize_mxfp4", x.data_ptr(), R, K, ldx, out.codes.data_ptr(),
                    out.scales.data_ptr(), _stream(x.device))
     _lib.check("sharq_quantize_mxfp4", st)
     return out
