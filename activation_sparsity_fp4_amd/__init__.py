@@ -231,7 +231,12 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
             out = MXFP4(torch.empty((E, stages(K), R, 64), dtype=torch.uint8, device=x.device),
                         torch.empty((E, stages(K), R, 4), dtype=torch.uint8, device=x.device), K)
         for e in range(E):
-            quantize_mxfp4(x[e], MXFP4(out.codes[e], out.scales[e], K))
+            scales = out.scales[e]
+            # the library wants a scale block on a 16-byte boundary; in a stack of odd sizes it may lie off one
+            block = torch.empty_like(scales) if scales.data_ptr() % 16 else scales
+            quantize_mxfp4(x[e], MXFP4(out.codes[e], block, K))
+            if block is not scales:
+                scales.copy_(block)
         return out
     _need(x, torch.bfloat16, "x", 2)
     if x.stride(1) != 1:
