@@ -125,6 +125,11 @@ def _same_device(first, *others):
             raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
 
 
+def _parts(prep):
+    """The tensors of a Prepared or NVPrepared that an entry point reads or writes."""
+    return prep.bb_codes, prep.bb_scales, prep.res_codes, prep.res_scales, prep.mask
+
+
 def _run(name, device, *args):
     """Enqueue an entry point on the device's current stream and raise on a bad status."""
     torch = _torch()
@@ -202,15 +207,15 @@ def prepare(x, gamma=None, n: int = 2, m: int = 4, with_mask: bool = True, out: 
         _need(out.rms_scale, torch.float32, "rms_scale", 1)
         if out.rms_scale.numel() != T or not out.rms_scale.is_contiguous():
             raise ValueError("rms_scale must be a contiguous fp32 [T] tensor")
-        st = _lib.call("sharq_prepare_rms", x.data_ptr(), T, K, x.stride(0), _ptr(gamma), float(rms_eps), n, m,
-                       out.rms_scale.data_ptr(), out.bb_codes.data_ptr(), out.bb_scales.data_ptr(),
-                       out.res_codes.data_ptr(), out.res_scales.data_ptr(), _ptr(out.mask), _stream(x.device))
-        _lib.check("sharq_prepare_rms", st)
+        _same_device(x, gamma, *_parts(out), out.rms_scale)
+        _run("sharq_prepare_rms", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), float(rms_eps), n, m,
+             out.rms_scale.data_ptr(), out.bb_codes.data_ptr(), out.bb_scales.data_ptr(),
+             out.res_codes.data_ptr(), out.res_scales.data_ptr(), _ptr(out.mask))
         return out
-    st = _lib.call("sharq_prepare", x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m,
-                   out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
-                   out.res_scales.data_ptr(), _ptr(out.mask), _stream(x.device))
-    _lib.check("sharq_prepare", st)
+    _same_device(x, gamma, *_parts(out))
+    _run("sharq_prepare", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m,
+         out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
+         out.res_scales.data_ptr(), _ptr(out.mask))
     return out
 
 
@@ -259,9 +264,9 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
         _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, ldx, _ptr(gamma),
              float(rms_eps), 0, out.codes.data_ptr(), out.scales.data_ptr())
         return out
-    st = _lib.call("sharq_quantize_mxfp4", x.data_ptr(), R, K, ldx, out.codes.data_ptr(),
-                   out.scales.data_ptr(), _stream(x.device))
-    _lib.check("sharq_quantize_mxfp4", st)
+    _same_device(x, out.codes, out.scales)
+    _run("sharq_quantize_mxfp4", x.device, x.data_ptr(), R, K, ldx, out.codes.data_ptr(),
+         out.scales.data_ptr())
     return out
 
 
@@ -297,18 +302,17 @@ def linear(prep: Prepared, w: MXFP4, out=None, split_k: bool = True):
     if out is None:
         out = torch.empty((T, O), dtype=torch.float32, device=prep.bb_codes.device)
     _check_matrix(out, torch.float32, T, O, "out")
+    _same_device(*_parts(prep), w.codes, w.scales, out)
     nbytes = _lib.call("sharq_linear_workspace_bytes", T, O, K) if split_k else 0
     if nbytes > 0:
         ws = _workspace(out.device, nbytes)
-        st = _lib.call("sharq_linear_ws", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
-                       prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-                       T, O, K, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel(), _stream(out.device))
-        _lib.check("sharq_linear_ws", st)
+        _run("sharq_linear_ws", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
+             prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+             T, O, K, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
         return out
-    st = _lib.call("sharq_linear", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(), prep.res_codes.data_ptr(),
-                   prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), T, O, K,
-                   out.data_ptr(), out.stride(0), _stream(out.device))
-    _lib.check("sharq_linear", st)
+    _run("sharq_linear", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(), prep.res_codes.data_ptr(),
+         prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), T, O, K,
+         out.data_ptr(), out.stride(0))
     return out
 
 
@@ -328,10 +332,10 @@ def linear_scratchfree(prep: Prepared, w: MXFP4, out):
         raise ValueError("weight K does not match the activation K")
     _check_stage_major(w.codes, w.scales, O, K, "w")
     _check_matrix(out, torch.float32, T, O, "out")
-    st = _lib.call("sharq_linear_scratchfree", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
-                   prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-                   T, O, K, out.data_ptr(), out.stride(0), _stream(out.device))
-    _lib.check("sharq_linear_scratchfree", st)
+    _same_device(*_parts(prep), w.codes, w.scales, out)
+    _run("sharq_linear_scratchfree", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
+         prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+         T, O, K, out.data_ptr(), out.stride(0))
     return out
 
 
@@ -358,11 +362,10 @@ def linear_grouped(prep: Prepared, w: MXFP4, seg_offsets, a_rows=None, out=None)
     if out is None:
         out = torch.empty((P, O), dtype=torch.float32, device=w.codes.device)
     _check_matrix(out, torch.float32, P, O, "out", contiguous=True)
-    st = _lib.call("sharq_linear_grouped", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
-                   prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), prep.bb_codes.shape[1], _ptr(a_rows),
-                   seg_offsets.data_ptr(), E, w.codes.data_ptr(), w.scales.data_ptr(), P, O, K, out.data_ptr(),
-                   _stream(out.device))
-    _lib.check("sharq_linear_grouped", st)
+    _same_device(*_parts(prep), w.codes, w.scales, seg_offsets, a_rows, out)
+    _run("sharq_linear_grouped", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
+         prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), prep.bb_codes.shape[1], _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w.codes.data_ptr(), w.scales.data_ptr(), P, O, K, out.data_ptr())
     return out
 
 
@@ -415,14 +418,13 @@ def _fused_call(prep, w_gu, T, I, K, n, m, h, hp, split_k):
             prep.res_scales.data_ptr(), w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), T, I, K, n, m, _ptr(h),
             _ptr(hp and hp.bb_codes), _ptr(hp and hp.bb_scales), _ptr(hp and hp.res_codes),
             _ptr(hp and hp.res_scales), _ptr(hp and hp.mask))
+    _same_device(*_parts(prep), w_gu.codes, w_gu.scales, h, *(_parts(hp) if hp else ()))
     nbytes = _lib.call("sharq_linear_silu_prepare_workspace_bytes", T, I, K) if split_k else 0
     if nbytes > 0:
         ws = _workspace(dev, nbytes)
-        st = _lib.call("sharq_linear_silu_prepare_ws", *args, ws.data_ptr(), ws.numel(), _stream(dev))
-        _lib.check("sharq_linear_silu_prepare_ws", st)
+        _run("sharq_linear_silu_prepare_ws", dev, *args, ws.data_ptr(), ws.numel())
         return
-    st = _lib.call("sharq_linear_silu_prepare", *args, _stream(dev))
-    _lib.check("sharq_linear_silu_prepare", st)
+    _run("sharq_linear_silu_prepare", dev, *args)
 
 
 def linear_grouped_silu_prepare(prep: Prepared, w_gu: MXFP4, seg_offsets, a_rows=None, n: int = 2, m: int = 4,
@@ -465,12 +467,12 @@ def linear_grouped_silu_prepare(prep: Prepared, w_gu: MXFP4, seg_offsets, a_rows
         hp = Prepared(torch.empty((G, P, 64), **kw), torch.empty((G, P, 4), **kw),
                       torch.empty((G, P, 64), **kw), torch.empty((G, P, 4), **kw),
                       torch.empty((P, I // 8), **kw) if with_mask else None, I)
-    st = _lib.call("sharq_linear_grouped_silu_prepare", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
-                   prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), prep.bb_codes.shape[1], _ptr(a_rows),
-                   seg_offsets.data_ptr(), E, w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), P, I, K, n, m, _ptr(h),
-                   _ptr(hp and hp.bb_codes), _ptr(hp and hp.bb_scales), _ptr(hp and hp.res_codes),
-                   _ptr(hp and hp.res_scales), _ptr(hp and hp.mask), _stream(dev))
-    _lib.check("sharq_linear_grouped_silu_prepare", st)
+    _same_device(*_parts(prep), w_gu.codes, w_gu.scales, seg_offsets, a_rows, h, *(_parts(hp) if hp else ()))
+    _run("sharq_linear_grouped_silu_prepare", dev, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
+         prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), prep.bb_codes.shape[1], _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), P, I, K, n, m, _ptr(h),
+         _ptr(hp and hp.bb_codes), _ptr(hp and hp.bb_scales), _ptr(hp and hp.res_codes),
+         _ptr(hp and hp.res_scales), _ptr(hp and hp.mask))
     return hp, h
 
 
@@ -500,9 +502,9 @@ def compress_backbone(prep: Prepared, n: int = 2, m: int = 4, out: CompactBackbo
                               torch.empty((T, row), dtype=torch.uint8, device=dev), n, m, K)
     if tuple(out.codes.shape) != (T, K // 4) or tuple(out.meta.shape) != (T, row) or (out.n, out.m, out.K) != (n, m, K):
         raise ValueError("out does not match the backbone")
-    st = _lib.call("sharq_compress_backbone", prep.bb_codes.data_ptr(), prep.mask.data_ptr(), T, K, n, m,
-                   out.codes.data_ptr(), out.meta.data_ptr(), _stream(prep.bb_codes.device))
-    _lib.check("sharq_compress_backbone", st)
+    _same_device(prep.bb_codes, prep.mask, out.codes, out.meta)
+    _run("sharq_compress_backbone", prep.bb_codes.device, prep.bb_codes.data_ptr(), prep.mask.data_ptr(), T, K, n, m,
+         out.codes.data_ptr(), out.meta.data_ptr())
     return out
 
 
@@ -525,9 +527,9 @@ def expand_backbone(cb: CompactBackbone, bb_codes=None, mask=None, with_mask: bo
         raise ValueError(f"bb_codes must be a contiguous [{stages(K)}, {T}, 64] tensor")
     if mask is not None:
         _check_matrix(mask, torch.uint8, T, K // 8, "mask", contiguous=True)
-    st = _lib.call("sharq_expand_backbone", cb.codes.data_ptr(), cb.meta.data_ptr(), T, K, cb.n, cb.m,
-                   bb_codes.data_ptr(), _ptr(mask), _stream(dev))
-    _lib.check("sharq_expand_backbone", st)
+    _same_device(cb.codes, cb.meta, bb_codes, mask)
+    _run("sharq_expand_backbone", dev, cb.codes.data_ptr(), cb.meta.data_ptr(), T, K, cb.n, cb.m,
+         bb_codes.data_ptr(), _ptr(mask))
     return bb_codes, mask
 
 
@@ -550,14 +552,13 @@ def moe_combine(y, pair_index, weights, out=None, bf16: bool = False):
     if out is None:
         out = torch.empty((T, H), dtype=dt, device=y.device)
     _check_matrix(out, dt, T, H, "out", contiguous=True)
+    _same_device(y, pair_index, weights, out)
     if rows_bf16:
-        _same_device(y, pair_index, weights, out)
         _run("sharq_moe_combine_bf16", y.device, y.data_ptr(), P, H, pair_index.data_ptr(), weights.data_ptr(), T, k,
              0 if bf16 else out.data_ptr(), out.data_ptr() if bf16 else 0)
         return out
-    st = _lib.call("sharq_moe_combine", y.data_ptr(), P, H, pair_index.data_ptr(), weights.data_ptr(), T, k,
-                   0 if bf16 else out.data_ptr(), out.data_ptr() if bf16 else 0, _stream(y.device))
-    _lib.check("sharq_moe_combine", st)
+    _run("sharq_moe_combine", y.device, y.data_ptr(), P, H, pair_index.data_ptr(), weights.data_ptr(), T, k,
+         0 if bf16 else out.data_ptr(), out.data_ptr() if bf16 else 0)
     return out
 
 
@@ -572,8 +573,8 @@ def silu_mul(gu, out=None):
     if out is None:
         out = torch.empty((T, I), dtype=torch.bfloat16, device=gu.device)
     _check_matrix(out, torch.bfloat16, T, I, "out", contiguous=True)
-    st = _lib.call("sharq_silu_mul", gu.data_ptr(), T, I, out.data_ptr(), _stream(gu.device))
-    _lib.check("sharq_silu_mul", st)
+    _same_device(gu, out)
+    _run("sharq_silu_mul", gu.device, gu.data_ptr(), T, I, out.data_ptr())
     return out
 
 
@@ -643,10 +644,10 @@ def prepare_nvfp4(x, tensor_scale: float, gamma=None, n: int = 2, m: int = 4, wi
         if out.mask is not None:
             _check_matrix(out.mask, torch.uint8, T, K // 8, "out.mask", contiguous=True)
         out = out._replace(tensor_scale=float(tensor_scale))
-    st = _lib.call("sharq_prepare_nvfp4", x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m, float(tensor_scale),
-                   out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
-                   out.res_scales.data_ptr(), _ptr(out.mask), _stream(x.device))
-    _lib.check("sharq_prepare_nvfp4", st)
+    _same_device(x, gamma, *_parts(out))
+    _run("sharq_prepare_nvfp4", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m, float(tensor_scale),
+         out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
+         out.res_scales.data_ptr(), _ptr(out.mask))
     return out
 
 
@@ -663,9 +664,9 @@ def quantize_nvfp4(w, tensor_scale: float, out: Optional[NVFP4] = None) -> NVFP4
     else:
         _check_nv(out.codes, out.scales, O, K, "out")
         out = out._replace(tensor_scale=float(tensor_scale))
-    st = _lib.call("sharq_quantize_nvfp4", w.data_ptr(), O, K, w.stride(0), float(tensor_scale),
-                   out.codes.data_ptr(), out.scales.data_ptr(), _stream(w.device))
-    _lib.check("sharq_quantize_nvfp4", st)
+    _same_device(w, out.codes, out.scales)
+    _run("sharq_quantize_nvfp4", w.device, w.data_ptr(), O, K, w.stride(0), float(tensor_scale),
+         out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 
@@ -682,11 +683,11 @@ def linear_nvfp4(prep: NVPrepared, w: NVFP4, out=None):
     if out is None:
         out = torch.empty((T, O), dtype=torch.float32, device=prep.bb_codes.device)
     _check_matrix(out, torch.float32, T, O, "out")
-    st = _lib.call("sharq_linear_nvfp4", prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
-                   prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), float(prep.tensor_scale),
-                   w.codes.data_ptr(), w.scales.data_ptr(), float(w.tensor_scale), T, O, K, out.data_ptr(),
-                   out.stride(0), _stream(out.device))
-    _lib.check("sharq_linear_nvfp4", st)
+    _same_device(*_parts(prep), w.codes, w.scales, out)
+    _run("sharq_linear_nvfp4", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
+         prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), float(prep.tensor_scale),
+         w.codes.data_ptr(), w.scales.data_ptr(), float(w.tensor_scale), T, O, K, out.data_ptr(),
+         out.stride(0))
     return out
 
 
@@ -705,9 +706,9 @@ def _pack(codes_rm, scales_rm, K, block, name):
     G = stages(K)
     codes = torch.empty((G, R, 64), dtype=torch.uint8, device=codes_rm.device)
     scales = torch.empty((G, R, 128 // block), dtype=torch.uint8, device=codes_rm.device)
-    st = _lib.call("sharq_pack_stage_major", codes_rm.data_ptr(), scales_rm.data_ptr(), R, K, block,
-                   codes.data_ptr(), scales.data_ptr(), _stream(codes_rm.device))
-    _lib.check("sharq_pack_stage_major", st)
+    _same_device(codes_rm, scales_rm)
+    _run("sharq_pack_stage_major", codes_rm.device, codes_rm.data_ptr(), scales_rm.data_ptr(), R, K, block,
+         codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -740,9 +741,9 @@ def unpack_stage_major(codes, scales, K: int):
     block = 128 // per
     codes_rm = torch.empty((R, K // 2), dtype=torch.uint8, device=codes.device)
     scales_rm = torch.empty((R, K // block), dtype=torch.uint8, device=codes.device)
-    st = _lib.call("sharq_unpack_stage_major", codes.data_ptr(), scales.data_ptr(), R, K, block,
-                   codes_rm.data_ptr(), scales_rm.data_ptr(), _stream(codes.device))
-    _lib.check("sharq_unpack_stage_major", st)
+    _same_device(codes, scales)
+    _run("sharq_unpack_stage_major", codes.device, codes.data_ptr(), scales.data_ptr(), R, K, block,
+         codes_rm.data_ptr(), scales_rm.data_ptr())
     return codes_rm, scales_rm
 
 
