@@ -270,24 +270,16 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
     return out
 
 
-_workspaces = {}
-
-
-def _workspace(device, nbytes):
-    """A device workspace of at least nbytes for split-K calls, cached per
-    (device, stream) so that calls on one stream (which never overlap) share it."""
+def _scratch(device, nbytes):
+    """Workspace of one call, from the allocator that orders it with the
+    stream's work (in a graph, from the graph's own memory); None for 0."""
     torch = _torch()
-    key = (device.index, _stream(device))
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
 
 
 def linear(prep: Prepared, w: MXFP4, out=None, split_k: bool = True):
     """Two-path FP4 GEMM: Y = deq(backbone) W^T + deq(residual) W^T, fp32 [T, O].
-    With split_k, K is split over a cached workspace (sharq_linear_ws) where
+    With split_k, K is split over a workspace (sharq_linear_ws) where
     the library's plan expects it to be faster (too few output tiles to fill
     the GPU, K long enough); the result is deterministic."""
     torch = _torch()
@@ -305,7 +297,7 @@ def linear(prep: Prepared, w: MXFP4, out=None, split_k: bool = True):
     _same_device(*_parts(prep), w.codes, w.scales, out)
     nbytes = _lib.call("sharq_linear_workspace_bytes", T, O, K) if split_k else 0
     if nbytes > 0:
-        ws = _workspace(out.device, nbytes)
+        ws = _scratch(out.device, nbytes)
         _run("sharq_linear_ws", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
              prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
              T, O, K, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
@@ -376,7 +368,7 @@ def linear_silu_prepare(prep: Prepared, w_gu: MXFP4, n: int = 2, m: int = 4, wit
     prepare(h, n, m). Returns (Prepared of h or None, h or None); the results
     equal linear(split_k) -> silu_mul -> prepare bit for bit. With split_k,
     problems with too few tiles to fill the GPU split K as linear does
-    (sharq_linear_silu_prepare_ws over the cached workspace)."""
+    (sharq_linear_silu_prepare_ws)."""
     torch = _torch()
     _check_prepared(prep)
     _need(w_gu.codes, torch.uint8, "w_gu.codes", 3)
@@ -421,7 +413,7 @@ def _fused_call(prep, w_gu, T, I, K, n, m, h, hp, split_k):
     _same_device(*_parts(prep), w_gu.codes, w_gu.scales, h, *(_parts(hp) if hp else ()))
     nbytes = _lib.call("sharq_linear_silu_prepare_workspace_bytes", T, I, K) if split_k else 0
     if nbytes > 0:
-        ws = _workspace(dev, nbytes)
+        ws = _scratch(dev, nbytes)
         _run("sharq_linear_silu_prepare_ws", dev, *args, ws.data_ptr(), ws.numel())
         return
     _run("sharq_linear_silu_prepare", dev, *args)
@@ -789,13 +781,6 @@ def _out_dtype(out, dtype):
 def _workspace_bytes(name, *shape):
     """The library's answer for a shape (asking it takes a fifth of a small call)."""
     return _lib.call(name, *shape)
-
-
-def _scratch(device, nbytes):
-    """Workspace of one call, from the allocator that orders it with the
-    stream's work (in a graph, from the graph's own memory); None for 0."""
-    torch = _torch()
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
 
 
 def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True):
