@@ -336,21 +336,11 @@ def linear_grouped(prep: Prepared, w: MXFP4, seg_offsets, a_rows=None, out=None)
     seg_offsets int32 [E+1]; a_rows int32 [P] (source row of each sorted pair) or None."""
     torch = _torch()
     _check_prepared(prep)
-    _need(w.codes, torch.uint8, "w.codes", 4)
-    _need(w.scales, torch.uint8, "w.scales", 4)
-    _need(seg_offsets, torch.int32, "seg_offsets", 1)
-    E, _, O, _ = w.codes.shape
+    E, _, O, _ = _check_mx(w, "w", 4)
     K = prep.K
     if w.K != K:
         raise ValueError("weight K does not match the activation K")
-    _check_stage_major(w.codes[0], w.scales[0], O, K, "w")
-    if seg_offsets.numel() != E + 1:
-        raise ValueError("seg_offsets must have E + 1 entries")
-    if a_rows is not None:
-        _need(a_rows, torch.int32, "a_rows", 1)
-        P = a_rows.numel()
-    else:
-        P = prep.bb_codes.shape[1]
+    P = _check_plan(seg_offsets, E, a_rows, prep.bb_codes.shape[1])
     if out is None:
         out = torch.empty((P, O), dtype=torch.float32, device=w.codes.device)
     _check_matrix(out, torch.float32, P, O, "out", contiguous=True)
@@ -429,21 +419,11 @@ def linear_grouped_silu_prepare(prep: Prepared, w_gu: MXFP4, seg_offsets, a_rows
     `out` (a Prepared of [G_I, P, ...]) receives prepare(h) when given."""
     torch = _torch()
     _check_prepared(prep)
-    _need(w_gu.codes, torch.uint8, "w_gu.codes", 4)
-    _need(w_gu.scales, torch.uint8, "w_gu.scales", 4)
-    _need(seg_offsets, torch.int32, "seg_offsets", 1)
-    E, _, O, _ = w_gu.codes.shape
+    E, _, O, _ = _check_mx(w_gu, "w_gu", 4)
     K = prep.K
     if w_gu.K != K or O % 2:
         raise ValueError("w_gu must be [E, 2I, K] with the activation's K")
-    _check_stage_major(w_gu.codes[0], w_gu.scales[0], O, K, "w_gu")
-    if seg_offsets.numel() != E + 1:
-        raise ValueError("seg_offsets must have E + 1 entries")
-    if a_rows is not None:
-        _need(a_rows, torch.int32, "a_rows", 1)
-        P = a_rows.numel()
-    else:
-        P = prep.bb_codes.shape[1]
+    P = _check_plan(seg_offsets, E, a_rows, prep.bb_codes.shape[1])
     I = O // 2
     dev = prep.bb_codes.device
     kw = dict(dtype=torch.uint8, device=dev)
@@ -837,22 +817,29 @@ def linear_silu_mxfp4(a: MXFP4, w_gu: MXFP4, out: Optional[MXFP4] = None, split_
     return out
 
 
+def _check_plan(seg_offsets, E, a_rows, rows):
+    """Output rows of a grouped call over `rows` activation rows: the segments and the gather lie side by side."""
+    torch = _torch()
+    _need(seg_offsets, torch.int32, "seg_offsets", 1)
+    if seg_offsets.numel() != E + 1 or not seg_offsets.is_contiguous():
+        raise ValueError("seg_offsets must be a contiguous [E + 1] tensor")
+    if a_rows is None:
+        return rows
+    _need(a_rows, torch.int32, "a_rows", 1)
+    if not a_rows.is_contiguous():
+        raise ValueError("a_rows must be contiguous")
+    return a_rows.numel()
+
+
 def _check_grouped(a, w, seg_offsets, a_rows, name):
     """(T_src, E, rows of the weight, P) of a grouped call on the plain path."""
-    torch = _torch()
     T = _check_mx(a, "a")[1]
     E, _, O, _ = _check_mx(w, name, 4)
     if w.K != a.K:
         raise ValueError("weight K does not match the activation K")
-    _need(seg_offsets, torch.int32, "seg_offsets", 1)
-    if seg_offsets.numel() != E + 1 or not seg_offsets.is_contiguous():
-        raise ValueError("seg_offsets must be a contiguous [E + 1] tensor")
-    if a_rows is not None:
-        _need(a_rows, torch.int32, "a_rows", 1)
-        if not a_rows.is_contiguous():
-            raise ValueError("a_rows must be contiguous")
+    P = _check_plan(seg_offsets, E, a_rows, T)
     _same_device(a.codes, a.scales, w.codes, w.scales, seg_offsets, a_rows)
-    return T, E, O, T if a_rows is None else a_rows.numel()
+    return T, E, O, P
 
 
 def linear_grouped_mxfp4(a: MXFP4, w: MXFP4, seg_offsets, a_rows=None, out=None, dtype=None):

@@ -1,0 +1,47 @@
+"""Arguments whose layout the kernels do not read are refused: strided segments
+and gathers, stacks of experts that are no contiguous block, outputs of another
+shape (CPU: the library calls are recorded, not made)."""
+
+import pytest
+import torch
+
+import activation_sparsity_fp4_amd as sq
+from host_stub import on_gpu, record
+from test_binding_devices import E, K, tensors, u8
+
+
+def _every_other(t):
+    """The values of t at a stride of 2."""
+    wide = torch.zeros(2 * t.numel(), dtype=t.dtype)
+    return on_gpu(wide.as_strided((t.numel(),), (2,)))
+
+
+def _stacks(w):
+    """Stacks [E, ..] of w's shape that are not one contiguous block: one expert for all, and a slice of every other."""
+    G, R = w.codes.shape[1:3]
+    one = sq.MXFP4(on_gpu(torch.zeros(1, G, R, 64, dtype=torch.uint8).expand(E, G, R, 64)), w.scales, K)
+    two = sq.MXFP4(w.codes, on_gpu(torch.zeros(2 * E, G, R, 4, dtype=torch.uint8).as_strided(
+        (E, G, R, 4), (2 * G * R * 4, R * 4, 4, 1))), K)
+    return one, two, sq.MXFP4(w.codes, u8(E - 1, G, R, 4, index=0), K)
+
+
+CALLS = {"linear_grouped": (sq.linear_grouped, "prep", "we"),
+         "linear_grouped_silu_prepare": (sq.linear_grouped_silu_prepare, "prep", "gue"),
+         "linear_grouped_mxfp4": (sq.linear_grouped_mxfp4, "mx", "we"),
+         "linear_grouped_silu_mxfp4": (sq.linear_grouped_silu_mxfp4, "mx", "gue")}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_grouped(monkeypatch, name):
+    calls = record(monkeypatch, sq)
+    f, a, w = CALLS[name]
+    t = tensors(0)
+    a, w, seg, rows = t[a], t[w], t["seg"], t["rows"]
+    f(a, w, seg, rows)
+    assert len(calls) == 1
+    bad = [(a, w, _every_other(seg), rows), (a, w, seg, _every_other(rows)),
+           (a, w, on_gpu(torch.zeros(E, dtype=torch.int32)), rows)]
+    for args in bad + [(a, s, seg, rows) for s in _stacks(w)]:
+        with pytest.raises(ValueError):
+            f(*args)
+    assert len(calls) == 1
