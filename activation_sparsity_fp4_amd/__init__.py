@@ -387,6 +387,7 @@ def linear_silu_prepare_into(prep: Prepared, w_gu: MXFP4, out: Prepared, n: int 
     """linear_silu_prepare writing prepare(h) into preallocated `out` (no h)."""
     _check_prepared(prep)
     _check_prepared(out)
+    _check_mx(w_gu, "w_gu")
     T, K, I = prep.bb_codes.shape[1], prep.K, out.K
     if w_gu.K != K or tuple(w_gu.codes.shape) != (stages(K), 2 * I, 64) or out.bb_codes.shape[1] != T:
         raise ValueError("shapes of prep, w_gu and out do not match")

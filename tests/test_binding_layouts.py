@@ -7,7 +7,7 @@ import torch
 
 import activation_sparsity_fp4_amd as sq
 from host_stub import on_gpu, record
-from test_binding_devices import E, K, tensors, u8
+from test_binding_devices import E, K, O, tensors, u8
 
 
 def _every_other(t):
@@ -45,3 +45,16 @@ def test_grouped(monkeypatch, name):
         with pytest.raises(ValueError):
             f(*args)
     assert len(calls) == 1
+
+
+def test_silu_prepare_into(monkeypatch):
+    calls = record(monkeypatch, sq)
+    t = tensors(0)
+    gu, g = t["gu"], sq.stages(K)
+    for bad in (gu._replace(scales=u8(g, O, 4, index=0)), gu._replace(scales=gu.scales.as_subclass(torch.Tensor)),
+                gu._replace(codes=on_gpu(torch.zeros(g, 4 * O, 64, dtype=torch.uint8)[:, ::2]))):
+        with pytest.raises(ValueError):
+            sq.linear_silu_prepare_into(t["prep"], bad, t["hp"])
+    with pytest.raises(TypeError):
+        sq.linear_silu_prepare_into(t["prep"], gu._replace(scales=on_gpu(gu.scales.float())), t["hp"])
+    assert not calls
