@@ -473,8 +473,10 @@ def compress_backbone(prep: Prepared, n: int = 2, m: int = 4, out: CompactBackbo
         dev = prep.bb_codes.device
         out = CompactBackbone(torch.empty((T, K // 4), dtype=torch.uint8, device=dev),
                               torch.empty((T, row), dtype=torch.uint8, device=dev), n, m, K)
-    if tuple(out.codes.shape) != (T, K // 4) or tuple(out.meta.shape) != (T, row) or (out.n, out.m, out.K) != (n, m, K):
+    if (out.n, out.m, out.K) != (n, m, K):
         raise ValueError("out does not match the backbone")
+    _check_matrix(out.codes, torch.uint8, T, K // 4, "out.codes", contiguous=True)
+    _check_matrix(out.meta, torch.uint8, T, row, "out.meta", contiguous=True)
     _same_device(prep.bb_codes, prep.mask, out.codes, out.meta)
     _run("sharq_compress_backbone", prep.bb_codes.device, prep.bb_codes.data_ptr(), prep.mask.data_ptr(), T, K, n, m,
          out.codes.data_ptr(), out.meta.data_ptr())
@@ -488,6 +490,10 @@ def expand_backbone(cb: CompactBackbone, bb_codes=None, mask=None, with_mask: bo
     _need(cb.codes, torch.uint8, "codes", 2)
     _need(cb.meta, torch.uint8, "meta", 2)
     T, K = cb.codes.shape[0], cb.K
+    row = _lib.call("sharq_backbone_meta_row_bytes", K, cb.n, cb.m)
+    _lib.check("sharq_backbone_meta_row_bytes", int(min(row, 0)))
+    _check_matrix(cb.codes, torch.uint8, T, K // 4, "codes", contiguous=True)
+    _check_matrix(cb.meta, torch.uint8, T, row, "meta", contiguous=True)
     dev = cb.codes.device
     if bb_codes is None:
         bb_codes = torch.empty((stages(K), T, 64), dtype=torch.uint8, device=dev)

@@ -7,7 +7,7 @@ import torch
 
 import activation_sparsity_fp4_amd as sq
 from host_stub import on_gpu, record
-from test_binding_devices import E, K, O, tensors, u8
+from test_binding_devices import E, K, O, T, tensors, u8
 
 
 def _every_other(t):
@@ -57,4 +57,23 @@ def test_silu_prepare_into(monkeypatch):
             sq.linear_silu_prepare_into(t["prep"], bad, t["hp"])
     with pytest.raises(TypeError):
         sq.linear_silu_prepare_into(t["prep"], gu._replace(scales=on_gpu(gu.scales.float())), t["hp"])
+    assert not calls
+
+
+def test_compact_backbone(monkeypatch):
+    calls = record(monkeypatch, sq)
+    t = tensors(0)
+    cb, row = t["cb"], t["cb"].meta.shape[1]
+    strided = lambda n: on_gpu(torch.zeros(T, 2 * n, dtype=torch.uint8)[:, :n])  # noqa: E731
+    for bad in (cb._replace(codes=strided(K // 4)), cb._replace(meta=strided(row))):
+        with pytest.raises(ValueError):
+            sq.compress_backbone(t["prep"], out=bad)
+        with pytest.raises(ValueError):
+            sq.expand_backbone(bad)
+    for bad in (cb._replace(codes=u8(T, K // 4 - 1, index=0)), cb._replace(meta=u8(T, row - 1, index=0)),
+                cb._replace(meta=u8(T - 1, row, index=0))):
+        with pytest.raises(ValueError):
+            sq.expand_backbone(bad)
+    with pytest.raises(TypeError):
+        sq.compress_backbone(t["prep"], out=cb._replace(meta=on_gpu(cb.meta.int())))
     assert not calls
