@@ -235,6 +235,12 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
         if out is None:
             out = MXFP4(torch.empty((E, stages(K), R, 64), dtype=torch.uint8, device=x.device),
                         torch.empty((E, stages(K), R, 4), dtype=torch.uint8, device=x.device), K)
+        elif out.K != K:
+            raise ValueError("out was allocated for another K")
+        _need(out.codes, torch.uint8, "out.codes", 4)
+        _need(out.scales, torch.uint8, "out.scales", 4)
+        if out.codes.shape[0] != E or out.scales.shape[0] != E:
+            raise ValueError(f"out must hold {E} experts")
         for e in range(E):
             scales = out.scales[e]
             # the library wants a scale block on a 16-byte boundary; in a stack of odd sizes it may lie off one
@@ -251,6 +257,8 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
     if out is None:
         out = MXFP4(torch.empty((stages(K), R, 64), dtype=torch.uint8, device=x.device),
                     torch.empty((stages(K), R, 4), dtype=torch.uint8, device=x.device), K)
+    elif out.K != K:
+        raise ValueError("out was allocated for another K")
     _need(out.codes, torch.uint8, "out.codes", 3)
     _need(out.scales, torch.uint8, "out.scales", 3)
     _check_stage_major(out.codes, out.scales, R, K, "out")

@@ -7,7 +7,7 @@ import torch
 
 import activation_sparsity_fp4_amd as sq
 from host_stub import on_gpu, record
-from test_binding_devices import E, K, O, T, tensors, u8
+from test_binding_devices import E, K, O, P, T, tensors, u8
 
 
 def _every_other(t):
@@ -77,3 +77,22 @@ def test_compact_backbone(monkeypatch):
     with pytest.raises(TypeError):
         sq.compress_backbone(t["prep"], out=cb._replace(meta=on_gpu(cb.meta.int())))
     assert not calls
+
+
+def test_stack_outputs(monkeypatch):
+    """quantize_mxfp4 of a stack writes an output of as many experts and of that K."""
+    calls = record(monkeypatch, sq)
+    x = on_gpu(torch.zeros(E, O, K, dtype=torch.bfloat16))
+    w = tensors(0)["we"]
+    sq.quantize_mxfp4(x, w)
+    assert len(calls) == E
+    g = sq.stages(K)
+    for bad in (sq.MXFP4(u8(E + 1, g, O, 64, index=0), u8(E + 1, g, O, 4, index=0), K),
+                sq.MXFP4(w.codes, u8(E + 1, g, O, 4, index=0), K),
+                sq.MXFP4(u8(E - 1, g, O, 64, index=0), u8(E - 1, g, O, 4, index=0), K), w._replace(K=K - 32)):
+        with pytest.raises(ValueError):
+            sq.quantize_mxfp4(x, bad)
+    with pytest.raises(ValueError):
+        sq.quantize_mxfp4(on_gpu(torch.zeros(T, K, dtype=torch.bfloat16)), tensors(0)["mx"]._replace(K=K - 32))
+    assert len(calls) == E
+    assert P == T  # the outputs above stand for pairs as well
