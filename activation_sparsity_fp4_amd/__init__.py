@@ -106,6 +106,11 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _ld(t):
+    """Leading dimension of a [rows, columns] tensor; a single row has none, whatever stride it reports."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _need(t, dtype, name, ndim=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
@@ -208,12 +213,12 @@ def prepare(x, gamma=None, n: int = 2, m: int = 4, with_mask: bool = True, out: 
         if out.rms_scale.numel() != T or not out.rms_scale.is_contiguous():
             raise ValueError("rms_scale must be a contiguous fp32 [T] tensor")
         _same_device(x, gamma, *_parts(out), out.rms_scale)
-        _run("sharq_prepare_rms", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), float(rms_eps), n, m,
+        _run("sharq_prepare_rms", x.device, x.data_ptr(), T, K, _ld(x), _ptr(gamma), float(rms_eps), n, m,
              out.rms_scale.data_ptr(), out.bb_codes.data_ptr(), out.bb_scales.data_ptr(),
              out.res_codes.data_ptr(), out.res_scales.data_ptr(), _ptr(out.mask))
         return out
     _same_device(x, gamma, *_parts(out))
-    _run("sharq_prepare", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m,
+    _run("sharq_prepare", x.device, x.data_ptr(), T, K, _ld(x), _ptr(gamma), n, m,
          out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
          out.res_scales.data_ptr(), _ptr(out.mask))
     return out
@@ -253,7 +258,6 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
     if x.stride(1) != 1:
         raise ValueError("x rows must be contiguous along K")
     R, K = x.shape
-    ldx = x.stride(0) if R > 1 else K
     if out is None:
         out = MXFP4(torch.empty((stages(K), R, 64), dtype=torch.uint8, device=x.device),
                     torch.empty((stages(K), R, 4), dtype=torch.uint8, device=x.device), K)
@@ -269,11 +273,11 @@ def quantize_mxfp4(x, out: Optional[MXFP4] = None, gamma=None, rms_eps: Optional
                 raise ValueError(f"gamma must hold K = {K} entries, got {gamma.numel()}")
             gamma = gamma.contiguous()
         _same_device(x, gamma, out.codes, out.scales)
-        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, ldx, _ptr(gamma),
+        _run("sharq_quantize_mxfp4_rms", x.device, x.data_ptr(), R, K, _ld(x), _ptr(gamma),
              float(rms_eps), 0, out.codes.data_ptr(), out.scales.data_ptr())
         return out
     _same_device(x, out.codes, out.scales)
-    _run("sharq_quantize_mxfp4", x.device, x.data_ptr(), R, K, ldx, out.codes.data_ptr(),
+    _run("sharq_quantize_mxfp4", x.device, x.data_ptr(), R, K, _ld(x), out.codes.data_ptr(),
          out.scales.data_ptr())
     return out
 
@@ -308,11 +312,11 @@ def linear(prep: Prepared, w: MXFP4, out=None, split_k: bool = True):
         ws = _scratch(out.device, nbytes)
         _run("sharq_linear_ws", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
              prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-             T, O, K, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
+             T, O, K, out.data_ptr(), _ld(out), ws.data_ptr(), ws.numel())
         return out
     _run("sharq_linear", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(), prep.res_codes.data_ptr(),
          prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), T, O, K,
-         out.data_ptr(), out.stride(0))
+         out.data_ptr(), _ld(out))
     return out
 
 
@@ -335,7 +339,7 @@ def linear_scratchfree(prep: Prepared, w: MXFP4, out):
     _same_device(*_parts(prep), w.codes, w.scales, out)
     _run("sharq_linear_scratchfree", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
          prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-         T, O, K, out.data_ptr(), out.stride(0))
+         T, O, K, out.data_ptr(), _ld(out))
     return out
 
 
@@ -632,7 +636,7 @@ def prepare_nvfp4(x, tensor_scale: float, gamma=None, n: int = 2, m: int = 4, wi
             _check_matrix(out.mask, torch.uint8, T, K // 8, "out.mask", contiguous=True)
         out = out._replace(tensor_scale=float(tensor_scale))
     _same_device(x, gamma, *_parts(out))
-    _run("sharq_prepare_nvfp4", x.device, x.data_ptr(), T, K, x.stride(0), _ptr(gamma), n, m, float(tensor_scale),
+    _run("sharq_prepare_nvfp4", x.device, x.data_ptr(), T, K, _ld(x), _ptr(gamma), n, m, float(tensor_scale),
          out.bb_codes.data_ptr(), out.bb_scales.data_ptr(), out.res_codes.data_ptr(),
          out.res_scales.data_ptr(), _ptr(out.mask))
     return out
@@ -652,7 +656,7 @@ def quantize_nvfp4(w, tensor_scale: float, out: Optional[NVFP4] = None) -> NVFP4
         _check_nv(out.codes, out.scales, O, K, "out")
         out = out._replace(tensor_scale=float(tensor_scale))
     _same_device(w, out.codes, out.scales)
-    _run("sharq_quantize_nvfp4", w.device, w.data_ptr(), O, K, w.stride(0), float(tensor_scale),
+    _run("sharq_quantize_nvfp4", w.device, w.data_ptr(), O, K, _ld(w), float(tensor_scale),
          out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
@@ -674,7 +678,7 @@ def linear_nvfp4(prep: NVPrepared, w: NVFP4, out=None):
     _run("sharq_linear_nvfp4", out.device, prep.bb_codes.data_ptr(), prep.bb_scales.data_ptr(),
          prep.res_codes.data_ptr(), prep.res_scales.data_ptr(), float(prep.tensor_scale),
          w.codes.data_ptr(), w.scales.data_ptr(), float(w.tensor_scale), T, O, K, out.data_ptr(),
-         out.stride(0))
+         _ld(out))
     return out
 
 
@@ -793,7 +797,7 @@ def linear_mxfp4(a: MXFP4, w: MXFP4, out=None, dtype=None, split_k: bool = True)
         out, ldy = torch.empty((T, O), dtype=dtype, device=dev), O
     else:
         _check_matrix(out, dtype, T, O, "out")
-        ldy = out.stride(0) if T > 1 else O
+        ldy = _ld(out)
     _same_device(a.codes, a.scales, w.codes, w.scales, out)
     ws = _scratch(dev, _workspace_bytes("sharq_linear_mxfp4_workspace_bytes", T, O, K) if split_k else 0)
     _run("sharq_linear_mxfp4", dev, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
@@ -960,7 +964,7 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     r = Routing(expert, weight.view(torch.float32), torch.empty(E + 1, dtype=torch.int32, device=dev),
                 a_rows.view(-1), pair_index)
     ws = _scratch(dev, _workspace_bytes("sharq_moe_route_workspace_bytes", T, E)) if T > 1 else None
-    _run("sharq_moe_route", dev, logits.data_ptr(), kind, T, E, logits.stride(0) if T > 1 else E, _ptr(bias), k,
+    _run("sharq_moe_route", dev, logits.data_ptr(), kind, T, E, _ld(logits), _ptr(bias), k,
          _SCORES[score], groups, groups if top_groups is None else top_groups, _GROUP_SCORES[group_score],
          int(renormalize), float(scale), _ptr(num_tokens), expert.data_ptr(), weight.data_ptr(),
          r.seg_offsets.data_ptr(), a_rows.data_ptr(), pair_index.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
