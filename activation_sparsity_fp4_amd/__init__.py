@@ -931,8 +931,9 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     groups > 1 only the top_groups best groups of consecutive experts take
     part, judged by their largest value ("max") or the sum of their two largest
     scores + bias ("sum2"). weight is the score without the bias, divided by
-    the sum over the chosen with renormalize, times scale. Rows from
-    num_tokens (int32 [1] on the device) on are padding and choose nothing."""
+    the sum over the chosen with renormalize, times scale (held in float32, as
+    the weights are). Rows from num_tokens (int32 [1] on the device) on are
+    padding and choose nothing."""
     torch = _torch()
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")

@@ -594,7 +594,8 @@ SHARQ_API int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint
  * Outputs:
  *  expert  i32 [T][k], best first; -1 where fewer than k could be chosen.
  *  weight  fp32 [T][k]: s (without the bias), divided by the sum over the
- *          chosen if renormalize, times scale; float64 inside, one rounding.
+ *          chosen if renormalize, times scale; float64 inside, one rounding
+ *          (scale itself is fp32).
  *          0 in an empty slot.
  *  seg_offsets i32 [E+1], a_rows i32 [T k]: the pairs (token, expert) sorted
  *          by expert, tokens in order inside one; a_rows[p] is the token of

@@ -273,3 +273,11 @@ def test_values_closer_than_float32_tells(sq, T, E, k, groups, top, score, gscor
     run(sq, x, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=gscore)
     bias[rng.random(E) < 0.5] = 0.25
     run(sq, x, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=gscore, renormalize=False)
+
+
+@pytest.mark.parametrize("scale", [1.1, 0.1, -2.446, 1e-30, 0.0])
+def test_scale_is_held_in_float32(sq, scale):
+    """The factor is fp32's; the product with the float64 share is rounded once."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((30, 24)).astype(np.float32)
+    check(sq.moe_route(f32_to_gpu(x), 5, scale=scale), moe_route_ref(x, 5, scale=float(np.float32(scale))))
