@@ -434,10 +434,12 @@ constexpr int kRouteThreads = NE <= 8 ? 1024 : 512;
 // Routes the tokens of chunk blockIdx.x. LDS: bit masks, counts and places of
 // the experts, then k slots (with a bias k + 1) of every token in flight, then, with groups,
 // group_doubles of every token in flight. Bound by the chain of a token (load,
-// k rounds of a maximum over its lanes, float64 weights) at few tokens, by the
-// vector instructions of its rounds at many: 1 x 128, k = 8: 6.3 us; 4096 x
-// 128 bf16: 7.0 us; 16384 x 256 with bias and 4 of 8 groups: 29 us (16.8 MB
-// read, 2.1 MB written: 4 us at the rate of a copy).
+// k rounds of a maximum over its lanes, float64 weights) at few tokens: 1 x 128, k
+// = 8: 6.3 us; 4096 x 128 bf16: 7.0 us. At many by vector instructions and by
+// waiting, about half and half: 16384 x 256 with bias and 4 of 8 groups 27-28 us
+// (16.8 MB read, 2.1 MB written: 4 us at the rate of a copy) with 10.0k vector
+// instructions a SIMD, 17 us at four cycles each and 2.4 GHz. A CU holds one workgroup,
+// four waves a SIMD, and a wave waits for 55% of its cycles.
 template <int LANES, int NE, bool kBias>
 __global__ __launch_bounds__(kRouteThreads<NE>) void moe_route_kernel(RouteArgs a, int64_t chunk_tokens, int chunks) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];

@@ -544,9 +544,12 @@ __device__ __forceinline__ TileRows dense_rows(int64_t m0, int64_t T, int bm) {
   return tr;
 }
 
-// Many tokens: bound by the matrix cores at the clock that power allows with the
-// whole chip busy (2048 x 14336 x 4096, fp32 out: 61-65 us, 3.7-3.9 PFLOP/s,
-// where a loop of MFMAs on registers reaches 6.2-6.6). Few: by the weight's
+// Many tokens, as 2048 x 14336 x 4096 (65 us with fp32 out, 61 with bf16, 3.7-4.0
+// PFLOP/s): 256 tiles, so a CU has one workgroup of four waves, whose stage takes
+// 812 cycles where its MFMAs take 512, and the stores at the end overlap nothing
+// (11.9k of 103.6k cycles, 4.8k of 96.7k with bf16). The matrix cores are busy for
+// 54-58% of the cycles, at the 1.5-1.7 GHz that the chip holds then; a loop of MFMAs
+// on registers reaches 6.2-6.6 PFLOP/s at 1.55 GHz. Few tokens: by the weight's
 // bytes (57344 x 8192: 42 us, 6 TB/s), or by a workgroup's own chain of stages
 // (333 x 4128 x 1000: 9.4 us for 33 stages, 4 of them launch, first loads and
 // stores).
@@ -564,8 +567,11 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_linear_kerne
   mx_store<C, Out>(acc, lds, y, ldy, tr, n0, op.O, wide);
 }
 
-// Bound as above: 2048 x 4096 -> 2 x 14336 118 us (4.1 PFLOP/s), 8 x 8192 -> 2 x
-// 28672 41 us (6 TB/s of weights).
+// 2048 x 4096 -> 2 x 14336 118 us (4.1 PFLOP/s): two workgroups a CU, whose stages
+// take 1058 cycles together where their MFMAs take 1024; with the SiLU and coding
+// (8.1k of a workgroup's 42.6k cycles) and 1792 tiles on 512 places (3.5 rounds) the
+// matrix cores are busy for 66% of the cycles, at 1.47 GHz. 8 x 8192 -> 2 x 28672 41
+// us (6 TB/s of weights).
 template <class C>
 __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_linear_silu_kernel(MxOperands op, MxH out,
                                                                                     int tiles_m, int tiles_total) {
@@ -665,11 +671,15 @@ __device__ __forceinline__ void mx_select_expert(MxOperands& op, int e) {
   op.w_scales += (int64_t)e * op.O * 4 * op.nsteps;
 }
 
-// Per expert. Bound by the weights' bytes at few tokens, by MFMAs (partial row
-// tiles too: about a fifth more rows at 256 rows an expert) and the stores at
-// many. Qwen3-30B-A3B layer (128 experts, top 8, 2048 -> 2 x 768 -> 2048): 4
-// tokens gate|up 13.5 us, down 7-8; 512 tokens 42 and 28; 4096 tokens 92 and 70
-// (134 MB of bf16 rows).
+// Per expert. Bound by the weights' bytes at few tokens. At many a workgroup's ends
+// weigh, for K is short: Qwen3-30B-A3B layer (128 experts, top 8, 2048 -> 2 x 768 ->
+// 2048) with 4096 tokens, cycles of a workgroup (two a CU): gate|up 3.4k until the
+// tile is found, 24.8k for 16 stages with the ring's first fill (1551 a stage), 5.5k
+// for SiLU and coding; down 2.8k, 11.8k for 6 stages (1966 each), 4.8k for the
+// stores of bf16 rows (134 MB in all, 28 us at the rate of a copy). The row tiles
+// hold 1.26 times the pairs. The matrix cores are busy for 40% and 24% of the
+// cycles. 4 tokens gate|up 13.5 us, down 7-8; 512 tokens 42 and 28; 4096 tokens
+// 80-105 and 62-78 with weights from the last-level cache or from memory.
 template <class C, class Out>
 __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void mx_grouped_kernel(
     MxOperands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, Out* __restrict__ y,
@@ -756,11 +766,11 @@ struct MxPlan {
 // constants are fitted to timed launches of all of them on 11 layer shapes from
 // 2048 x 768 to 57344 x 8192 (O x K), T = 1 .. 1024, whose best they pick but
 // for 1% on average and 13% at most. With 256 columns a tile alone the best was
-// 27% slower on average: 4096 x 4096 at T = 128 15.9 us, 64 x 64 tiles 8.9;
+// 22% slower on average: 4096 x 4096 at T = 128 15.9 us, 64 x 64 tiles 8.9;
 // 4096 x 14336 at T = 1024 49.9 us, 128 x 128 tiles 37.9; 28672 x 4096 at T = 1
 // 16.3 us, 64 x 128 tiles 12.8; and the other way round 57344 x 8192 at T = 1
 // 42 us, 45 to 50 with narrower tiles, 28672 x 4096 at T = 1024 72 us, 128 x 128
-// tiles 81. Split: 8192 x 28672 at T = 1 47 us whole, 24 us with S = 3.
+// tiles 81. Split: 8192 x 28672 at T = 1 47 us whole, 24.5 us with S = 4.
 MxPlan mx_plan(int64_t T, int64_t O, int64_t K, bool may_split) {
   const int64_t nsteps = ceil_div(K, 128);
   const int64_t s_max = !may_split || nsteps < 8 ? 1 : nsteps / 4 < kMxMaxSplits ? nsteps / 4 : kMxMaxSplits;

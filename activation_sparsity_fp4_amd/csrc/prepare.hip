@@ -368,11 +368,13 @@ __global__ __launch_bounds__(256) void prepare_rms_kernel(
 // ends with the tree's root). The wave roots meet in LDS and every wave
 // finishes the tree on its own: one barrier. A thread's first kHold blocks
 // stay in registers between the sum and the coding, later ones (K > 16384) are
-// read again. HBM-bound for many rows (2 bytes read and 0.53 written an
-// entry; 2048 x 4096: 8 us, 2.7 TB/s, the float64 sums and the coding take the
-// rest); for a few rows one round trip to memory and the 32 dependent float64
-// additions of a block (8 x 8192: 4.1 us; a block a lane as prepare_kernel
-// deals them: 9.8).
+// read again. Many rows: 2 bytes read and 0.53 written an entry, 2048 x 4096: 8-10
+// us from memory (4.4 at the rate of a copy), 6.6 with the input in the last-level
+// cache. Of those 6.6 the sums, which every block of the row waits for, take 1.6
+// (squares summed in float32 in place of float64 0.2 of it), the norm and the coding
+// 0.7; a workgroup has one row and nothing to do meanwhile. A few rows: one
+// round trip to memory and the 32 dependent float64 additions of a block (8 x 8192:
+// 4.1 us; a block a lane as prepare_kernel deals them: 9.8).
 template <bool kGamma, int kHold>
 __global__ __launch_bounds__(256) void quantize_rms_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                            const uint16_t* __restrict__ gamma, uint32_t K,
