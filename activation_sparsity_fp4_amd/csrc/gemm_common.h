@@ -96,6 +96,30 @@ __device__ __forceinline__ void buffer_to_lds4(i32x4 rsrc, uint32_t voff, uint32
                :: "v"(voff), "s"(rsrc), "s"(lds) : "memory", "m0");
 }
 
+// The same loads with the LDS address a sum formed in M0 itself: base + the
+// bytes that the template names.
+template <int BYTES>
+__device__ __forceinline__ void load_lds16(i32x4 rsrc, uint32_t voff, uint32_t base) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(base), "n"(BYTES) : "memory", "m0", "scc");
+}
+// One operand array: the buffer view of the stage to load next.
+struct StageView {
+  i32x4 r;
+  uint32_t stage_bytes;
+  __device__ __forceinline__ void start(const uint8_t* base, int64_t bytes, int stage) {
+    stage_bytes = (uint32_t)bytes;
+    r = make_rsrc(base + (int64_t)stage * bytes, bytes);
+  }
+  // On to the next stage; without one, to a view of nothing.
+  __device__ __forceinline__ void advance(bool live) {
+    const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + stage_bytes;
+    r[0] = (int)(uint32_t)at;
+    r[1] = (int)(uint32_t)(at >> 32);
+    r[2] = live ? (int)stage_bytes : 0;
+  }
+};
+
 // s_waitcnt with only the vector-memory counter bounded (gfx9 encoding).
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {

@@ -156,40 +156,11 @@ __device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, const MxScales<C>& 
                                                               (int)c.w[j], 2 * SUB, (int)c.a[i]);
 }
 
-// Buffer loads into LDS as in gemm_common.h, the LDS address a sum formed in
-// M0 itself: base + the bytes that the template names.
-template <int BYTES>
-__device__ __forceinline__ void load_lds16(i32x4 rsrc, uint32_t voff, uint32_t base) {
-  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(base), "n"(BYTES) : "memory", "m0", "scc");
-}
-__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(base) : "memory", "m0");
-}
-
-// One operand array: the buffer view of the stage to load next.
-struct MxView {
-  i32x4 r;
-  uint32_t stage_bytes;
-  __device__ __forceinline__ void start(const uint8_t* base, int64_t bytes, int stage) {
-    stage_bytes = (uint32_t)bytes;
-    r = make_rsrc(base + (int64_t)stage * bytes, bytes);
-  }
-  // On to the next stage; without one, to a view of nothing.
-  __device__ __forceinline__ void advance(bool live) {
-    const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + stage_bytes;
-    r[0] = (int)(uint32_t)at;
-    r[1] = (int)(uint32_t)(at >> 32);
-    r[2] = live ? (int)stage_bytes : 0;
-  }
-};
-
 // The loads of a wave; kDword: its scale load is a dword a lane. Every array's view moves on right behind its last load
 // of a stage, so that the scalar work is spread between the MFMAs too.
 template <class C, bool kDword>
 struct MxLoader {
-  MxView a, w, s;               // codes; the scales that the wave loads
+  StageView a, w, s;               // codes; the scales that the wave loads
   uint32_t a_off[C::kAChunks];  // byte offset of this lane's A code chunk inside a stage, kOOB if absent
   uint32_t w_off[C::kWChunks];
   uint32_t s_off;               // this lane's scale dwords
@@ -209,7 +180,7 @@ struct MxLoader {
       if constexpr (J == C::kCodeLoads - 1) w.advance(left > 0);
     } else {
       if constexpr (kDword)
-        load_lds4(s.r, s_off, ring + at + s_lds);
+        buffer_to_lds4(s.r, s_off, ring + at + s_lds);
       else
         load_lds16<0>(s.r, s_off, ring + at + s_lds);
       s.advance(left > 0);
