@@ -12,6 +12,10 @@ The plain MXFP4 path (one operand, no decomposition) and expert routing:
 
     y = linear_mxfp4(quantize_mxfp4(x), wq)        # fp32 or bf16 [T, O]
     r = moe_route(logits, k)                       # experts, weights, dispatch plan
+
+Layers at 8 bits (integer codes, a scale for each token and output channel):
+
+    y = linear_int8(quantize_int8(x), quantize_int8(w))
 """
 
 from __future__ import annotations
@@ -50,6 +54,14 @@ __all__ = [
     "linear_silu_mxfp4",
     "linear_grouped_mxfp4",
     "linear_grouped_silu_mxfp4",
+    "Int8",
+    "quantize_int8",
+    "pack_int8",
+    "unpack_int8",
+    "linear_int8",
+    "linear_silu_int8",
+    "linear_grouped_int8",
+    "linear_grouped_silu_int8",
     "Routing",
     "moe_route",
     "SharqError",
@@ -897,6 +909,234 @@ def linear_grouped_silu_mxfp4(a: MXFP4, w_gu: MXFP4, seg_offsets, a_rows=None,
     _run("sharq_linear_grouped_silu_mxfp4", a.codes.device, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
          seg_offsets.data_ptr(), E, w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), P, O // 2, a.K,
          out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer path: a scale for each token and each output channel
+# ---------------------------------------------------------------------------
+
+
+class Int8(NamedTuple):
+    """An 8-bit tensor: codes int8 [G, R, 64] with G = ceil(K / 64) (entry k of
+    row r at [k // 64, r, k % 64], zeros past K) and scales fp32 [R]; for expert
+    weights codes [E, G, O, 64] and scales [E, O]. An entry is code times scale."""
+    codes: "object"
+    scales: "object"
+    K: int
+
+
+def _int8_like(K, device, *rows):
+    """An Int8 tensor of [.., R, K] for rows (.., R)."""
+    torch = _torch()
+    return Int8(torch.empty((*rows[:-1], (K + 63) // 64, rows[-1], 64), dtype=torch.int8, device=device),
+                torch.empty(rows, dtype=torch.float32, device=device), K)
+
+
+def _check_int8(t, name, ndim=3):
+    """The shape of an Int8 tensor's codes; codes and scales are contiguous and fit its K."""
+    torch = _torch()
+    codes, scales, K = t
+    G = (K + 63) // 64
+    if type(codes) is type(scales) is torch.Tensor:
+        shape = codes.shape
+        if (len(shape) == ndim and shape[-3] == G and shape[-1] == 64 and scales.shape == (*shape[:-3], shape[-2])
+                and codes.dtype is torch.int8 and scales.dtype is torch.float32 and codes.is_cuda and scales.is_cuda
+                and codes.is_contiguous() and scales.is_contiguous()):
+            return shape
+    _need(codes, torch.int8, name + ".codes", ndim)
+    _need(scales, torch.float32, name + ".scales", ndim - 2)
+    shape = codes.shape
+    if shape[-3] != G or shape[-1] != 64 or tuple(scales.shape) != (*shape[:-3], shape[-2]):
+        raise ValueError(f"{name}: expected codes [.., {G}, R, 64] and scales [.., R], "
+                         f"got {tuple(shape)} and {tuple(scales.shape)}")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous")
+    return shape
+
+
+def _check_int8_out(out, K, device, *rows):
+    """out, or a new Int8 tensor of [.., R, K]."""
+    if out is None:
+        return _int8_like(K, device, *rows)
+    if out.K != K:
+        raise ValueError("out was allocated for another K")
+    shape = _check_int8(out, "out", len(rows) + 2)
+    if (*shape[:-3], shape[-2]) != rows:
+        raise ValueError(f"out must be an Int8 tensor of {list(rows)} rows")
+    return out
+
+
+def quantize_int8(x, out: Optional[Int8] = None, gamma=None, rms_eps: Optional[float] = None) -> Int8:
+    """8-bit codes of each row of x [R, K] (an activation [T, K], a weight [O, K])
+    or of a stack of expert weights [E, O, K]: scale = amax / 127, codes rounded
+    to nearest (ties to even). x is float32, bfloat16 or float16; rows may be
+    strided. A row that holds a NaN or an infinity has scale NaN and codes 0.
+    With rms_eps the rows of a bfloat16 [R, K] tensor are RMS-normed first
+    (per-row 1/rms, then gamma when given), as prepare(rms_eps=...) norms them."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if gamma is not None and rms_eps is None:
+        raise ValueError("gamma is the weight of the norm: it needs rms_eps")
+    dtype = torch.bfloat16 if rms_eps is not None else x.dtype
+    kind = 0 if dtype == torch.float32 else 1 if dtype == torch.bfloat16 else 2 if dtype == torch.float16 else None
+    if kind is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {dtype}")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must have 2 or 3 dims")
+    if x.dim() == 3 and rms_eps is not None:
+        raise ValueError("the norm is for [R, K] activations")
+    _need(x, dtype, "x")
+    R, K = x.shape[-2:]
+    if K < 1:
+        raise ValueError("x must have at least one column")
+    if x.numel() and K > 1 and x.stride(-1) != 1:
+        raise ValueError("x rows must be contiguous along K")
+    if x.dim() == 3:
+        E = x.shape[0]
+        ldx = x.stride(1) if R > 1 else x.stride(0) if E > 1 else K
+        if E > 1 and R > 1 and x.stride(0) != R * ldx:
+            x, ldx = x.contiguous(), K
+        rows = (E, R)
+    else:
+        E, ldx, rows = 1, _ld(x), (R,)
+    out = _check_int8_out(out, K, x.device, *rows)
+    if rms_eps is None:
+        _same_device(x, out.codes, out.scales)
+        _run("sharq_quantize_int8", x.device, x.data_ptr(), kind, E, R, K, ldx, out.codes.data_ptr(),
+             out.scales.data_ptr())
+        return out
+    if gamma is not None:
+        _need(gamma, torch.bfloat16, "gamma", 1)
+        if gamma.numel() != K:  # the kernels read K entries of gamma
+            raise ValueError(f"gamma must hold K = {K} entries, got {gamma.numel()}")
+        gamma = gamma.contiguous()
+    _same_device(x, gamma, out.codes, out.scales)
+    _run("sharq_quantize_int8_rms", x.device, x.data_ptr(), R, K, ldx, _ptr(gamma), float(rms_eps), 0,
+         out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+def pack_int8(codes_rm, scales) -> Int8:
+    """An Int8 tensor from row-major codes int8 [R, K] (or [E, R, K]) and scales
+    fp32 [R] ([E, R]), e.g. a weight quantised elsewhere. The scales are used as
+    they are."""
+    torch = _torch()
+    if not isinstance(codes_rm, torch.Tensor) or codes_rm.dim() not in (2, 3):
+        raise ValueError("codes must be a [R, K] or [E, R, K] tensor")
+    _need(codes_rm, torch.int8, "codes")
+    _need(scales, torch.float32, "scales", codes_rm.dim() - 1)
+    *rows, K = codes_rm.shape
+    if K < 1 or list(scales.shape) != rows:
+        raise ValueError(f"expected scales {rows} for codes {list(codes_rm.shape)}, got {list(scales.shape)}")
+    if not (codes_rm.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
+    _same_device(codes_rm, scales)
+    out = _int8_like(K, codes_rm.device, *rows)._replace(scales=scales)
+    _run("sharq_pack_int8", codes_rm.device, codes_rm.data_ptr(), rows[0] if len(rows) == 2 else 1, rows[-1], K,
+         out.codes.data_ptr())
+    return out
+
+
+def unpack_int8(t: Int8):
+    """The row-major codes int8 [R, K] (or [E, R, K]) of an Int8 tensor."""
+    torch = _torch()
+    shape = _check_int8(t, "t", 4 if isinstance(t.codes, torch.Tensor) and t.codes.dim() == 4 else 3)
+    rows = (*shape[:-3], shape[-2])
+    codes_rm = torch.empty((*rows, t.K), dtype=torch.int8, device=t.codes.device)
+    _same_device(t.codes, t.scales)
+    _run("sharq_unpack_int8", t.codes.device, t.codes.data_ptr(), rows[0] if len(rows) == 2 else 1, rows[-1], t.K,
+         codes_rm.data_ptr())
+    return codes_rm
+
+
+def linear_int8(a: Int8, w: Int8, out=None, dtype=None, bias=None):
+    """Y[t, o] = (sum over k of the codes' products) * a.scales[t] * w.scales[o]
+    (+ bias[o], fp32 [O]), [T, O] of dtype float32 (the default) or bfloat16 (the
+    fp32 value rounded once). The sum is exact, K < 131072."""
+    torch = _torch()
+    T, O, K = _check_int8(a, "a")[1], _check_int8(w, "w")[1], a.K
+    if w.K != K:
+        raise ValueError("weight K does not match the activation K")
+    dtype, number = _out_dtype(out, dtype)
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.numel() != O or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous [{O}] tensor")
+    dev = a.codes.device
+    if out is None:
+        out, ldy = torch.empty((T, O), dtype=dtype, device=dev), O
+    else:
+        _check_matrix(out, dtype, T, O, "out")
+        ldy = _ld(out)
+    _same_device(a.codes, a.scales, w.codes, w.scales, bias, out)
+    _run("sharq_linear_int8", dev, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+         _ptr(bias), T, O, K, out.data_ptr(), ldy, number)
+    return out
+
+
+def linear_silu_int8(a: Int8, w_gu: Int8, out: Optional[Int8] = None) -> Int8:
+    """Fused gate|up projection at 8 bits: the product with w_gu (I gate rows, then
+    I up rows), h = bf16(silu(gate) * up), 8-bit codes of h [T, I]. Equals
+    linear_int8 -> silu_mul -> quantize_int8 bit for bit (I a multiple of 8 there)."""
+    T, O, K = _check_int8(a, "a")[1], _check_int8(w_gu, "w_gu")[1], a.K
+    if w_gu.K != K or O % 2 or O == 0:
+        raise ValueError("w_gu must be [2I, K] with the activation's K")
+    I = O // 2
+    dev = a.codes.device
+    out = _check_int8_out(out, I, dev, T)
+    _same_device(a.codes, a.scales, w_gu.codes, w_gu.scales, out.codes, out.scales)
+    ws = _scratch(dev, _workspace_bytes("sharq_linear_silu_int8_workspace_bytes", T, I))
+    _run("sharq_linear_silu_int8", dev, a.codes.data_ptr(), a.scales.data_ptr(), w_gu.codes.data_ptr(),
+         w_gu.scales.data_ptr(), T, I, K, out.codes.data_ptr(), out.scales.data_ptr(), _ptr(ws),
+         0 if ws is None else ws.numel())
+    return out
+
+
+def _check_grouped_int8(a, w, seg_offsets, a_rows, name):
+    """(T_src, E, rows of the weight, P) of a grouped call at 8 bits."""
+    T = _check_int8(a, "a")[1]
+    E, _, O, _ = _check_int8(w, name, 4)
+    if w.K != a.K:
+        raise ValueError("weight K does not match the activation K")
+    P = _check_plan(seg_offsets, E, a_rows, T)
+    _same_device(a.codes, a.scales, w.codes, w.scales, seg_offsets, a_rows)
+    return T, E, O, P
+
+
+def linear_grouped_int8(a: Int8, w: Int8, seg_offsets, a_rows=None, out=None, dtype=None):
+    """linear_int8 per expert segment: row p of the [P, O] result (float32 or
+    bfloat16) is activation row a_rows[p] (row p without a_rows) times the
+    weight of the expert e with seg_offsets[e] <= p < seg_offsets[e + 1].
+    w.codes is [E, G, O, 64]. Rows of no segment are not written."""
+    torch = _torch()
+    T, E, O, P = _check_grouped_int8(a, w, seg_offsets, a_rows, "w")
+    dtype, number = _out_dtype(out, dtype)
+    if out is None:
+        out = torch.empty((P, O), dtype=dtype, device=a.codes.device)
+    else:
+        _check_matrix(out, dtype, P, O, "out", contiguous=True)
+        _same_device(a.codes, out)
+    _run("sharq_linear_grouped_int8", a.codes.device, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w.codes.data_ptr(), w.scales.data_ptr(), P, O, a.K, out.data_ptr(), number)
+    return out
+
+
+def linear_grouped_silu_int8(a: Int8, w_gu: Int8, seg_offsets, a_rows=None, out: Optional[Int8] = None) -> Int8:
+    """linear_silu_int8 per expert segment: 8-bit codes of h [P, I] for expert
+    weights w_gu.codes [E, G, 2I, 64]. Rows of no segment are not written."""
+    T, E, O, P = _check_grouped_int8(a, w_gu, seg_offsets, a_rows, "w_gu")
+    if O % 2 or O == 0:
+        raise ValueError("w_gu must be [E, 2I, K]")
+    I = O // 2
+    dev = a.codes.device
+    out = _check_int8_out(out, I, dev, P)
+    _same_device(a.codes, out.codes, out.scales)
+    ws = _scratch(dev, _workspace_bytes("sharq_linear_silu_int8_workspace_bytes", P, I))
+    _run("sharq_linear_grouped_silu_int8", dev, a.codes.data_ptr(), a.scales.data_ptr(), T, _ptr(a_rows),
+         seg_offsets.data_ptr(), E, w_gu.codes.data_ptr(), w_gu.scales.data_ptr(), P, I, a.K, out.codes.data_ptr(),
+         out.scales.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 

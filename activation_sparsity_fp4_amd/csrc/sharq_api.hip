@@ -489,6 +489,157 @@ int sharq_linear_grouped_silu_mxfp4(const uint8_t* a_codes, const uint8_t* a_sca
   return hip_status(sharq::launch_mx_grouped_silu(m, a_rows, seg_offsets, E, P, h_codes, h_scales, stream));
 }
 
+namespace {
+
+constexpr int64_t kMaxI8K = (int64_t)1 << 17;  // 2^14 a product of two codes: sums below 2^31
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_i8_rows(int64_t E, int64_t R, int64_t K) {
+  if (E < 0 || R < 0 || K <= 0) return SHARQ_EINVAL;
+  if (K >= kMaxI8K) return SHARQ_ENOTIMPL;
+  if (R >= kMaxMxRows || E >= ((int64_t)1 << 31) || E * R >= ((int64_t)1 << 31)) return SHARQ_EINVAL;
+  return SHARQ_OK;
+}
+
+int check_i8(int64_t rows, int64_t O, int64_t K) {
+  const int rc = check_i8_rows(1, rows, K);
+  return rc != SHARQ_OK ? rc : check_i8_rows(1, O, K);
+}
+
+bool i8_null(const sharq::I8Product& m) { return !m.a_codes || !m.a_scales || !m.w_codes || !m.w_scales; }
+bool i8_aligned(const sharq::I8Product& m) {
+  return aligned16(m.a_codes) && aligned16(m.w_codes) && aligned4(m.a_scales) && aligned4(m.w_scales) &&
+         aligned4(m.bias);
+}
+
+int check_i8_grouped(const sharq::I8Product& m, const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
+                     int64_t P) {
+  const int rc = check_i8(m.rows, m.O, m.K);
+  if (rc != SHARQ_OK) return rc;
+  if (E < 1 || P < 0 || P >= ((int64_t)1 << 31) || (!a_rows && m.rows < P)) return SHARQ_EINVAL;
+  if (!sharq::i8_grouped_fits(P, E, m.O)) return SHARQ_EINVAL;
+  if (P == 0 || m.O == 0) return SHARQ_OK;
+  if (i8_null(m) || !seg_offsets) return SHARQ_EINVAL;
+  if (!i8_aligned(m) || !aligned4(seg_offsets) || !aligned4(a_rows)) return SHARQ_EALIGN;
+  return SHARQ_OK;
+}
+
+// The coded h and the workspace of a gate|up call with rows.
+int check_i8_h(int64_t rows, int64_t I, const int8_t* h_codes, const float* h_scales, const void* workspace,
+               int64_t workspace_bytes) {
+  if (!h_codes || !h_scales || !workspace || workspace_bytes < sharq::i8_silu_workspace_bytes(rows, I))
+    return SHARQ_EINVAL;
+  return aligned16(h_codes) && aligned4(h_scales) && aligned16(workspace) ? SHARQ_OK : SHARQ_EALIGN;
+}
+
+int check_i8_silu_shape(int64_t rows, int64_t I, const void* workspace, int64_t workspace_bytes) {
+  if (I <= 0 || I >= kMaxMxRows / 2 || rows < 0 || rows >= kMaxMxRows) return SHARQ_EINVAL;
+  if (I >= kMaxI8K) return SHARQ_ENOTIMPL;  // h is coded for a product over I
+  return check_workspace(workspace, workspace_bytes);
+}
+
+}  // namespace
+
+int sharq_quantize_int8(const void* x, int dtype, int64_t E, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                        float* scales, hipStream_t stream) {
+  const int rc = check_i8_rows(E, R, K);
+  if (rc != SHARQ_OK) return rc;
+  if ((dtype != SHARQ_F32 && dtype != SHARQ_BF16 && dtype != SHARQ_F16) || ldx < K) return SHARQ_EINVAL;
+  if (E == 0 || R == 0) return SHARQ_OK;
+  if (!x || !codes || !scales) return SHARQ_EINVAL;
+  if (((uintptr_t)x & (dtype == SHARQ_F32 ? 3u : 1u)) || !aligned16(codes) || !aligned4(scales)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_quantize_int8(x, dtype, E, R, K, ldx, codes, scales, nullptr, 0, stream));
+}
+
+int sharq_quantize_int8_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma, float eps,
+                            float* rms_scale, int8_t* codes, float* scales, hipStream_t stream) {
+  const int rc = check_i8_rows(1, T, K);
+  if (rc != SHARQ_OK) return rc;
+  if (ldx < K || !(eps > 0.0f) || !(eps < INFINITY)) return SHARQ_EINVAL;
+  if (T == 0) return SHARQ_OK;
+  if (!x || !codes || !scales) return SHARQ_EINVAL;
+  if (((uintptr_t)x & 1u) || ((uintptr_t)gamma & 1u) || !aligned4(rms_scale) || !aligned16(codes) || !aligned4(scales))
+    return SHARQ_EALIGN;
+  return hip_status(sharq::launch_quantize_int8_rms(x, T, K, ldx, gamma, eps, rms_scale, codes, scales, stream));
+}
+
+int sharq_pack_int8(const int8_t* codes_rm, int64_t E, int64_t R, int64_t K, int8_t* codes, hipStream_t stream) {
+  const int rc = check_i8_rows(E, R, K);
+  if (rc != SHARQ_OK) return rc;
+  if (E == 0 || R == 0) return SHARQ_OK;
+  if (!codes_rm || !codes) return SHARQ_EINVAL;
+  if (!aligned16(codes)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_pack_int8(codes_rm, E, R, K, codes, false, nullptr, stream));
+}
+
+int sharq_unpack_int8(const int8_t* codes, int64_t E, int64_t R, int64_t K, int8_t* codes_rm, hipStream_t stream) {
+  const int rc = check_i8_rows(E, R, K);
+  if (rc != SHARQ_OK) return rc;
+  if (E == 0 || R == 0) return SHARQ_OK;
+  if (!codes_rm || !codes) return SHARQ_EINVAL;
+  if (!aligned16(codes)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_pack_int8(nullptr, E, R, K, const_cast<int8_t*>(codes), true, codes_rm, stream));
+}
+
+int sharq_linear_int8(const int8_t* a_codes, const float* a_scales, const int8_t* w_codes, const float* w_scales,
+                      const float* bias, int64_t T, int64_t O, int64_t K, void* y, int64_t ldy, int dtype,
+                      hipStream_t stream) {
+  const sharq::I8Product m{a_codes, a_scales, w_codes, w_scales, bias, T, O, K};
+  const int rc = check_i8(T, O, K);
+  if (rc != SHARQ_OK) return rc;
+  if (ldy < O || (dtype != SHARQ_F32 && dtype != SHARQ_BF16) || !sharq::i8_linear_fits(T, O)) return SHARQ_EINVAL;
+  if (T == 0 || O == 0) return SHARQ_OK;
+  if (i8_null(m) || !y) return SHARQ_EINVAL;
+  if (!i8_aligned(m) || !aligned16(y)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_i8_linear(m, y, ldy, dtype == SHARQ_BF16, stream));
+}
+
+int64_t sharq_linear_silu_int8_workspace_bytes(int64_t T, int64_t I) {
+  if (check_i8_silu_shape(T, I, nullptr, 0) != SHARQ_OK) return 0;
+  return sharq::i8_silu_workspace_bytes(T, I);
+}
+
+int sharq_linear_silu_int8(const int8_t* a_codes, const float* a_scales, const int8_t* w_codes, const float* w_scales,
+                           int64_t T, int64_t I, int64_t K, int8_t* h_codes, float* h_scales, void* workspace,
+                           int64_t workspace_bytes, hipStream_t stream) {
+  int rc = check_i8_silu_shape(T, I, workspace, workspace_bytes);
+  if (rc != SHARQ_OK) return rc;
+  const sharq::I8Product m{a_codes, a_scales, w_codes, w_scales, nullptr, T, 2 * I, K};
+  if ((rc = check_i8(T, 2 * I, K)) != SHARQ_OK) return rc;
+  if (!sharq::i8_linear_fits(T, 2 * I + 64)) return SHARQ_EINVAL;  // 64: a partial last h tile
+  if (T == 0) return SHARQ_OK;
+  if (i8_null(m)) return SHARQ_EINVAL;
+  if ((rc = check_i8_h(T, I, h_codes, h_scales, workspace, workspace_bytes)) != SHARQ_OK) return rc;
+  if (!i8_aligned(m)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_i8_linear_silu(m, h_codes, h_scales, workspace, stream));
+}
+
+int sharq_linear_grouped_int8(const int8_t* a_codes, const float* a_scales, int64_t T_src, const int32_t* a_rows,
+                              const int32_t* seg_offsets, int32_t E, const int8_t* w_codes, const float* w_scales,
+                              int64_t P, int64_t O, int64_t K, void* y, int dtype, hipStream_t stream) {
+  const sharq::I8Product m{a_codes, a_scales, w_codes, w_scales, nullptr, T_src, O, K};
+  if (dtype != SHARQ_F32 && dtype != SHARQ_BF16) return SHARQ_EINVAL;
+  const int rc = check_i8_grouped(m, a_rows, seg_offsets, E, P);
+  if (rc != SHARQ_OK || P == 0 || O == 0) return rc;
+  if (!y) return SHARQ_EINVAL;
+  if (!aligned16(y)) return SHARQ_EALIGN;
+  return hip_status(sharq::launch_i8_grouped(m, a_rows, seg_offsets, E, P, y, dtype == SHARQ_BF16, stream));
+}
+
+int sharq_linear_grouped_silu_int8(const int8_t* a_codes, const float* a_scales, int64_t T_src, const int32_t* a_rows,
+                                   const int32_t* seg_offsets, int32_t E, const int8_t* w_codes,
+                                   const float* w_scales, int64_t P, int64_t I, int64_t K, int8_t* h_codes,
+                                   float* h_scales, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  int rc = check_i8_silu_shape(P, I, workspace, workspace_bytes);
+  if (rc != SHARQ_OK) return rc;
+  const sharq::I8Product m{a_codes, a_scales, w_codes, w_scales, nullptr, T_src, 2 * I, K};
+  rc = check_i8_grouped(m, a_rows, seg_offsets, E, P);
+  if (rc != SHARQ_OK || P == 0) return rc;
+  if ((rc = check_i8_h(P, I, h_codes, h_scales, workspace, workspace_bytes)) != SHARQ_OK) return rc;
+  return hip_status(sharq::launch_i8_grouped_silu(m, a_rows, seg_offsets, E, P, h_codes, h_scales, workspace, stream));
+}
+
 int64_t sharq_moe_route_workspace_bytes(int64_t T, int32_t E) {
   if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > 1024) return 0;
   return sharq::moe_route_workspace_bytes(T, E);

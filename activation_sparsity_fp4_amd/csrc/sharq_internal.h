@@ -133,6 +133,38 @@ struct RouteArgs {
 int64_t moe_route_workspace_bytes(int64_t T, int32_t E);
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
 
+// 8-bit integer coding (int8.hip). dtype as in the ABI (0 fp32, 1 bf16, 2 fp16);
+// seg (or null) bounds the rows that are written: [seg[0], seg[segments]).
+hipError_t launch_quantize_int8(const void* x, int dtype, int64_t E, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                                float* scales, const int32_t* seg, int32_t segments, hipStream_t stream);
+hipError_t launch_quantize_int8_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma,
+                                    float eps, float* rms_scale, int8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_pack_int8(const int8_t* codes_rm, int64_t E, int64_t R, int64_t K, int8_t* codes, bool unpack,
+                            int8_t* out_rm, hipStream_t stream);
+
+// Products of 8-bit codes (i8gemm.hip): activation [ceil(K/64)][rows][64] against
+// weight [ceil(K/64)][O][64] (grouped: one such tensor per expert).
+struct I8Product {
+  const int8_t* a_codes;
+  const float* a_scales;
+  const int8_t* w_codes;
+  const float* w_scales;
+  const float* bias;  // or null
+  int64_t rows, O, K;
+};
+constexpr int64_t kI8MaxWorkgroups = (int64_t)1 << 22;  // fewer than 2^32 threads
+bool i8_linear_fits(int64_t T, int64_t O);
+hipError_t launch_i8_linear(const I8Product& p, void* y, int64_t ldy, bool bf16, hipStream_t stream);
+// O = 2 I: gate rows, then up rows; the workspace holds h
+int64_t i8_silu_workspace_bytes(int64_t T, int64_t I);
+hipError_t launch_i8_linear_silu(const I8Product& p, int8_t* h_codes, float* h_scales, void* workspace,
+                                 hipStream_t stream);
+bool i8_grouped_fits(int64_t P, int32_t E, int64_t O);  // O: weight rows of an expert
+hipError_t launch_i8_grouped(const I8Product& p, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
+                             void* y, bool bf16, hipStream_t stream);
+hipError_t launch_i8_grouped_silu(const I8Product& p, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
+                                  int8_t* h_codes, float* h_scales, void* workspace, hipStream_t stream);
+
 hipError_t launch_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, const int32_t* pair_index,
                                    const float* weights, int64_t T, int k, float* out, uint16_t* out_bf16,
                                    hipStream_t stream);

@@ -626,6 +626,100 @@ SHARQ_API int sharq_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, co
                            const float* weights, int64_t T, int32_t k, float* out, uint16_t* out_bf16,
                            hipStream_t stream);
 
+/*
+ * 8-bit integer path: layers that stay at 8 bits next to the FP4 ones (one
+ * activation operand, codes of a byte, one fp32 scale for each token and each
+ * output channel).
+ *
+ * Coding of a row x' (fp32): s = fp32(amax / 127), the code of an entry the
+ * integer nearest to the exact quotient x' / s (ties to the even one), within
+ * [-127, 127]. A row of zeros has scale 0. A row that holds a NaN or an infinity
+ * has scale NaN and codes 0, so that its products are NaN (finite inputs are
+ * not required here).
+ * Layout: codes i8 [G][R][64] with G = ceil(K / 64): entry k of row r at
+ * [k / 64][r][k % 64]; bytes past K are zero. Scales fp32 [R]. Products take any
+ * codes of -128 .. 127 and any scales. K < 2^17 (the int32 sums; larger:
+ * SHARQ_ENOTIMPL), any K >= 1. Row counts and O < 2^25.
+ *
+ * sharq_quantize_int8 -- codes of x [E][R][ldx] of type dtype (SHARQ_F32,
+ * SHARQ_BF16, SHARQ_F16), the first K entries of each row: E tensors of R rows
+ * (an activation or a weight: E = 1; a stack of expert weights: E).
+ *  codes i8 [E][G][R][64], scales fp32 [E][R].
+ *  x needs the alignment of its type; rows that are 16-byte aligned with K a
+ *  multiple of 8 are read fastest. codes 16-byte aligned, scales 4. E R < 2^31.
+ * sharq_quantize_int8_rms -- the same of RMS-normed bf16 rows:
+ *   x' = bf16_rne(fp32(x) * r) * gamma, r = fp32(1 / sqrt(S / K + eps)) with S the
+ *   float64 sum of squares (gamma bf16 [K] may be NULL, 2-byte aligned).
+ *  rms_scale fp32 [T], written with r, or NULL. The sum's order is not
+ *  sharq_prepare_rms's, so r may differ from its in the last bit (where S / K +
+ *  eps lies within 2^-50 of a rounding border). eps finite and > 0.
+ */
+SHARQ_API int sharq_quantize_int8(const void* x, int dtype, int64_t E, int64_t R, int64_t K, int64_t ldx,
+                        int8_t* codes, float* scales, hipStream_t stream);
+SHARQ_API int sharq_quantize_int8_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma,
+                            float eps, float* rms_scale, int8_t* codes, float* scales, hipStream_t stream);
+
+/*
+ * sharq_pack_int8, sharq_unpack_int8 -- codes between row-major [E][R][K] (any
+ * alignment; what a quantiser elsewhere writes) and the layout above.
+ */
+SHARQ_API int sharq_pack_int8(const int8_t* codes_rm, int64_t E, int64_t R, int64_t K, int8_t* codes,
+                    hipStream_t stream);
+SHARQ_API int sharq_unpack_int8(const int8_t* codes, int64_t E, int64_t R, int64_t K, int8_t* codes_rm,
+                      hipStream_t stream);
+
+/*
+ * sharq_linear_int8 -- Y[t][o] = (sum_k qa[t][k] qw[o][k]) sa[t] sw[o] + bias[o].
+ *  a_codes i8 [G][T][64], a_scales fp32 [T]; w_codes i8 [G][O][64], w_scales
+ *  fp32 [O]; bias fp32 [O] or NULL.
+ *  y [T][ldy] of type dtype: SHARQ_F32 or SHARQ_BF16 (the fp32 value rounded to
+ *  nearest even). Any ldy >= O.
+ * The sum is exact; then one rounding to fp32, a product with sa and a fused one
+ * with sw and the bias (a sum times sa past fp32's range is an infinity, whatever
+ * sw). Codes and y 16-byte aligned, scales and bias 4.
+ * Requires ceil(T / 64) * ceil(O / 64) < 2^22.
+ */
+SHARQ_API int sharq_linear_int8(const int8_t* a_codes, const float* a_scales, const int8_t* w_codes,
+                      const float* w_scales, const float* bias, int64_t T, int64_t O, int64_t K, void* y, int64_t ldy,
+                      int dtype, hipStream_t stream);
+
+/*
+ * sharq_linear_silu_int8 -- a fused gate|up projection: sharq_linear_int8 against
+ * a weight of I gate rows followed by I up rows (fp32, no bias), h =
+ * bf16(silu(Y[t][i]) * Y[t][I + i]) (as sharq_silu_mul), and h coded as
+ * sharq_quantize_int8 codes it. Any I >= 1. h passes through the workspace, for a
+ * row's scale needs all of it.
+ *  h_codes i8 [ceil(I/64)][T][64], h_scales fp32 [T].
+ *  workspace  at least sharq_linear_silu_int8_workspace_bytes(T, I) bytes, 16-byte
+ *  aligned; overwritten. Calls that may overlap in time need separate ones.
+ */
+SHARQ_API int64_t sharq_linear_silu_int8_workspace_bytes(int64_t T, int64_t I);
+SHARQ_API int sharq_linear_silu_int8(const int8_t* a_codes, const float* a_scales, const int8_t* w_codes,
+                           const float* w_scales, int64_t T, int64_t I, int64_t K, int8_t* h_codes, float* h_scales,
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * sharq_linear_grouped_int8, sharq_linear_grouped_silu_int8 -- the two per expert
+ * segment, with the segments and the row gather of sharq_linear_grouped. Output
+ * row p is sorted pair p; rows of no segment are not written.
+ *  a_codes i8 [G][T_src][64], a_scales fp32 [T_src]; a_rows i32 [P] or NULL;
+ *  seg_offsets i32 [E+1]; w_codes i8 [E][G][O][64], w_scales fp32 [E][O] (O = 2 I
+ *  for the fused form); y [P][O]; h_codes i8 [ceil(I/64)][P][64], h_scales fp32 [P];
+ *  workspace as above for (P, I).
+ * Malformed segment or gather contents are handled as sharq_linear_grouped does
+ * (a gathered row outside [0, T_src) counts as zeros). Requires
+ * (P / 16 + min(P, E) + 1) * (O / 32 + 2) < 2^22 (workgroups).
+ */
+SHARQ_API int sharq_linear_grouped_int8(const int8_t* a_codes, const float* a_scales, int64_t T_src,
+                              const int32_t* a_rows, const int32_t* seg_offsets, int32_t E, const int8_t* w_codes,
+                              const float* w_scales, int64_t P, int64_t O, int64_t K, void* y, int dtype,
+                              hipStream_t stream);
+SHARQ_API int sharq_linear_grouped_silu_int8(const int8_t* a_codes, const float* a_scales, int64_t T_src,
+                                   const int32_t* a_rows, const int32_t* seg_offsets, int32_t E,
+                                   const int8_t* w_codes, const float* w_scales, int64_t P, int64_t I, int64_t K,
+                                   int8_t* h_codes, float* h_scales, void* workspace, int64_t workspace_bytes,
+                                   hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,3 +9,4 @@ from .sharq_ref import *  # noqa: F401,F403
 from .compact_ref import *  # noqa: F401,F403
 from .nvfp4_ref import *  # noqa: F401,F403
 from .plain_ref import *  # noqa: F401,F403
+from .int8_ref import *  # noqa: F401,F403
