@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsharq.so")
 SOURCES = ["prepare.hip", "gemm.hip", "glue.hip", "compact.hip", "nvfp4.hip", "layout.hip", "scratchfree.hip",
-           "mxgemm.hip", "moe_route.hip", "int8.hip", "i8gemm.hip", "sharq_api.hip"]
+           "mxgemm.hip", "moe_route.hip", "int8.hip", "i8gemm.hip", "i8grouped.hip", "sharq_api.hip"]
 CALIB_SOURCE = "calib.hip"
 CALIB_LIB = os.path.join(PKG, "libsharq_calib.so")
 ARCH = "gfx950"

@@ -1,370 +1,10 @@
-// Products of 8-bit integer codes with a scale for each token and each output
-// channel on gfx950 MFMA, dense or per expert segment:
-//   Y[t][o] = (sum_k qa[t][k] qw[o][k]) sa[t] sw[o] (+ bias[o]),
-// stored as fp32 or bf16, or, for a fused gate|up weight, turned into
-// h = bf16(silu(gate) * up). The sum is exact in int32 (K < 2^17), so no choice
-// of tile or of how K is divided changes a result.
-//
-// V_MFMA_I32_16X16X64_I8 takes 16 weight rows as its first operand and 16
-// activation rows as its second: lane l gives 16 bytes (K entries 16 (l / 16)
-// on) of row l % 16 of each, and its four accumulators are weight rows
-// 4 (l / 16) .. + 3 of token l % 16. On register operands it runs at 3.6-3.8
-// POP/s where V_MFMA_I32_32X32X32_I8 runs at 3.0-3.4: the chip's power sets the
-// clock, and this form draws less.
+// Dense products of 8-bit codes: kernels and the choice of a tile (i8gemm.h has
+// the products themselves).
 
-#include <utility>
-
-#include "gemm_common.h"
-#include "sharq_device.h"
-#include "sharq_internal.h"
-#include "silu.h"
+#include "i8gemm.h"
 
 namespace sharq {
 namespace {
-
-#define SHARQ_INLINE __attribute__((always_inline))
-
-// f(0), ..., f(N - 1) with the number as a compile-time constant.
-template <class F, int... I>
-__device__ __forceinline__ void static_for_each(F& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_each(f, std::make_integer_sequence<int, N>{});
-}
-template <int I>
-using int_c = std::integral_constant<int, I>;
-
-struct I8Operands {
-  const int8_t* a_codes;  // [G][rows][64]
-  const float* a_scales;  // [rows]
-  const int8_t* w_codes;  // [G][O][64] (grouped: already the expert's)
-  const float* w_scales;  // [O]
-  const float* bias;      // [O] or null
-  int64_t rows, O;
-  int nsteps;  // G
-};
-
-struct I8Out {
-  void* y;
-  int64_t ld;
-  bool wide;   // rows of y are 16-byte aligned
-  int64_t I;   // h columns of a gate|up product
-};
-
-// What a kernel makes of a tile's sums.
-enum I8Kind { kI8F32, kI8Bf16, kI8Silu };
-
-// ---------------------------------------------------------------------------
-// Tiles through LDS
-// ---------------------------------------------------------------------------
-
-// A workgroup tile of BM tokens x BN weight rows. Its waves stand in KS groups,
-// which divide K; the NWM x NWN waves of a group have WM x WN MFMA tiles of 16 x
-// 16 each. A group has a ring of RING LDS stages (64 K entries of the tile's rows);
-// WGS workgroups share a CU.
-template <int WM_, int WN_, int NWM_, int NWN_, int KS_, int RING_, int WGS_>
-struct I8Tile {
-  static constexpr int WM = WM_, WN = WN_, NWM = NWM_, NWN = NWN_, KS = KS_;
-  static constexpr int kGroup = NWM * NWN, kWaves = kGroup * KS, kThreads = 64 * kWaves;
-  static constexpr int BM = 16 * WM * NWM, BN = 16 * WN * NWN;
-  static constexpr int kOffW = BM * kRowBytes, kStage = (BM + BN) * kRowBytes;
-  static constexpr int kALoads = BM / 16 / kGroup, kWLoads = BN / 16 / kGroup, kLoads = kALoads + kWLoads;
-  static_assert(kALoads * 16 * kGroup == BM && kWLoads * 16 * kGroup == BN, "whole 1 KB chunks per wave");
-  static constexpr int kRing = RING_;
-  static constexpr int kRingBytes = KS * kRing * kStage;
-  static constexpr int kReduceBytes = (KS - 1) * BM * BN * 4;
-  static constexpr int kMain = kRingBytes > kReduceBytes ? kRingBytes : kReduceBytes;
-  // behind the ring: the tokens' scales, the weight rows' scales and biases
-  static constexpr int kScaleA = kMain, kScaleW = kScaleA + 4 * BM, kBias = kScaleW + 4 * BN;
-  static constexpr int kLds = kBias + 4 * BN;
-  static constexpr int kWavesPerSimd = (WGS_ * kWaves + 3) / 4;
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && WN % 2 == 0, "whole scale loads, columns in pairs");
-  static_assert(kRing >= 3 && WGS_ * (kLds + 64) <= kLdsBytes, "ring");
-};
-using I8x256x256 = I8Tile<8, 4, 2, 4, 1, 4, 1>;
-using I8x128x256 = I8Tile<4, 8, 2, 2, 1, 3, 2>;
-using I8x128x256k2 = I8Tile<4, 8, 2, 2, 2, 3, 1>;
-using I8x128x128 = I8Tile<4, 4, 2, 2, 1, 4, 2>;
-using I8x128x128k2 = I8Tile<4, 4, 2, 2, 2, 4, 1>;
-using I8x64x128k2 = I8Tile<2, 4, 2, 2, 2, 6, 1>;
-using I8x64x64k4 = I8Tile<2, 2, 2, 2, 4, 4, 1>;
-
-// LDS chunk swizzle for the 16-row fragments: a ds_read_b128 serves lanes 0-3,
-// 12-15, 20-23 and 24-27 (then 4-11, 16-19, 28-31, and the same from 32 on)
-// together. Those are, for each residue of the row by 4 (a quarter of the 64
-// banks), rows 4 q + r with q = 0, 3 of chunk c and q = 1, 2 of chunk c ^ 1; XOR
-// of the chunk with -q puts the four on different banks (no conflicts measured;
-// with +q, right for 32-row fragments, every read takes twice as long).
-__device__ __forceinline__ int i8_swz_part(int row) { return (-(row >> 2)) & 3; }
-__device__ __forceinline__ int i8_swz(int row, int part) {
-  return row * kRowBytes + ((part ^ i8_swz_part(row)) << 4);
-}
-
-// Weight rows behind the LDS rows of a tile, so that a lane's accumulators of
-// two (gate|up: four) neighbouring MFMA tiles are eight columns side by side:
-// 32 LDS rows are 32 output columns, row 16 j + r column 8 (r / 4) + 4 j + r % 4;
-// gate|up: 64 rows are gate (j even) and up (j odd) of 32 h columns, row
-// 16 j + r h column 8 (r / 4) + 4 (j / 2) + r % 4 (with two MFMA tiles a wave 32
-// rows are gate and up of 16 h columns, in order).
-template <class C, bool kSilu>
-struct I8Cols {
-  int64_t n0;  // first output (or h) column of the tile
-  int64_t n;   // output (or h) columns
-  static constexpr bool kEight = C::WN % 4 == 0;
-  __device__ __forceinline__ int64_t w_row(int x) const {  // -1 past the last column
-    const int j = x >> 4, r = x & 15;
-    if constexpr (!kSilu) {
-      const int64_t o = n0 + 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
-      return o < n ? o : -1;
-    } else {
-      const int64_t h = n0 + (kEight ? 32 * (j >> 2) + 8 * (r >> 2) + 4 * ((j >> 1) & 1) + (r & 3) : 16 * (j >> 1) + r);
-      return h < n ? h + ((j & 1) ? n : 0) : -1;
-    }
-  }
-};
-
-template <class C, int K>
-constexpr int kI8Cols = K == kI8Silu ? C::BN / 2 : C::BN;  // output (or h) columns of a tile
-
-// acc = the tile's sums; with KS groups, group q holds those of the WM rows i with
-// i % KS == q when it returns.
-//
-// An iteration multiplies the fragments of one stage, read in the one before,
-// and threads between its MFMAs the reads of the next stage's and the loads of
-// stage s + ring into the slot that stage s left: at its barrier every wave has
-// stage s in registers, and stage s + 1 has landed.
-template <class C, bool kSilu>
-__device__ __forceinline__ void i8_mainloop(const I8Operands& op, const TileRows& tr, const I8Cols<C, kSilu>& tc,
-                                            uint8_t* lds, v4i (&acc)[C::WM][C::WN]) {
-  const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kg = all / C::kGroup, wave = all % C::kGroup;
-  const int wm = wave % C::NWM, wn = wave / C::NWM, lr = lane & 15, lc = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j) acc[i][j] = v4i{};
-
-  // Scales and biases, 64 at a load: older than any stage's loads, so there before the first is read.
-  {
-    const i32x4 ra = make_rsrc(op.a_scales, op.rows * 4), rw = make_rsrc(op.w_scales, op.O * 4);
-    const i32x4 rb = make_rsrc(op.bias, op.bias ? op.O * 4 : 0);
-    constexpr int kA = C::BM / 64, kW = C::BN / 64;
-    const uint32_t base = lds_offset(lds + C::kScaleA);
-    for (int q = all; q < kA + 2 * kW; q += C::kWaves) {
-      const int x = 64 * (q < kA ? q : (q - kA) % kW) + lane;
-      const int64_t src = q < kA ? tr.src(x) : tc.w_row(x);
-      buffer_to_lds4(q < kA ? ra : q < kA + kW ? rw : rb, src >= 0 ? (uint32_t)(src * 4) : kOOB, base + 256 * q);
-    }
-  }
-
-  const int steps = (op.nsteps + C::KS - 1) / C::KS, first = kg * steps;
-  int left = op.nsteps - first < steps ? op.nsteps - first : steps;  // stages not yet issued
-  uint8_t* ring = lds + kg * C::kRing * C::kStage;
-  StageView va, vw;
-  va.start(reinterpret_cast<const uint8_t*>(op.a_codes), op.rows * kRowBytes, first);
-  vw.start(reinterpret_cast<const uint8_t*>(op.w_codes), op.O * kRowBytes, first);
-  if (left <= 0) va.r[2] = vw.r[2] = 0;
-  // A lane fills a fixed LDS chunk; it reads the global chunk that belongs there after the swizzle.
-  uint32_t a_off[C::kALoads], w_off[C::kWLoads];
-#pragma unroll
-  for (int j = 0; j < C::kALoads; ++j) {
-    const int row = 16 * (wave + C::kGroup * j) + (lane >> 2);
-    const int64_t src = tr.src(row);
-    a_off[j] = src >= 0 ? (uint32_t)(src * kRowBytes + ((lane & 3) ^ i8_swz_part(row)) * 16) : kOOB;
-  }
-#pragma unroll
-  for (int j = 0; j < C::kWLoads; ++j) {
-    const int row = 16 * (wave + C::kGroup * j) + (lane >> 2);
-    const int64_t src = tc.w_row(row);
-    w_off[j] = src >= 0 ? (uint32_t)(src * kRowBytes + ((lane & 3) ^ i8_swz_part(row)) * 16) : kOOB;
-  }
-  const uint32_t base = lds_offset(ring) + 1024 * wave;
-  uint32_t at = 0;
-  auto issue = [&](auto J) SHARQ_INLINE {
-    constexpr int j = decltype(J)::value;
-    const uint32_t to = __builtin_amdgcn_readfirstlane(base + at);
-    if constexpr (j < C::kALoads) {
-      load_lds16<1024 * C::kGroup * j>(va.r, a_off[j], to);
-      if constexpr (j == C::kALoads - 1) va.advance(--left > 0);
-    } else {
-      load_lds16<C::kOffW + 1024 * C::kGroup * (j - C::kALoads)>(vw.r, w_off[j - C::kALoads], to);
-      if constexpr (j == C::kLoads - 1) {
-        vw.advance(left > 0);
-        at = at + C::kStage == C::kRing * C::kStage ? 0 : at + C::kStage;
-      }
-    }
-  };
-#pragma unroll
-  for (int b = 0; b < C::kRing; ++b) static_for<C::kLoads>(issue);
-
-  v4i fa[2][C::WM], fw[2][C::WN];
-  constexpr int kReads = C::WM + C::WN, kMfmas = C::WM * C::WN;
-  auto read = [&](auto R, auto SET, const uint8_t* st) SHARQ_INLINE {
-    constexpr int r = decltype(R)::value, set = decltype(SET)::value;
-    if constexpr (r < C::WM)
-      fa[set][r] = *reinterpret_cast<const v4i*>(st + i8_swz(16 * (C::WM * wm + r) + lr, lc));
-    else if constexpr (r < kReads)
-      fw[set][r - C::WM] = *reinterpret_cast<const v4i*>(st + C::kOffW + i8_swz(16 * (C::WN * wn + r - C::WM) + lr, lc));
-  };
-  wait_vmcnt<(C::kRing - 1) * C::kLoads>();
-  ring_barrier();
-  static_for<kReads>([&](auto R) SHARQ_INLINE { read(R, int_c<0>{}, ring); });
-  const uint8_t* cur = ring;
-  // Reads go into the first 5/8 of the slots, so that the other MFMAs cover the latency of the last.
-  constexpr int kReadSlots = kMfmas * 5 / 8 < 1 ? 1 : kMfmas * 5 / 8, kPerSlot = (kReads + kReadSlots - 1) / kReadSlots;
-  auto body = [&](auto SET) SHARQ_INLINE {
-    constexpr int set = decltype(SET)::value;
-    const uint8_t* next = cur == ring + (C::kRing - 1) * C::kStage ? ring : cur + C::kStage;
-    wait_vmcnt<(C::kRing - 2) * C::kLoads>();  // the next stage landed; later ones may be in flight
-    ring_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
-    static_for<kMfmas>([&](auto M) SHARQ_INLINE {
-      constexpr int m = decltype(M)::value, i = m / C::WN, j = m % C::WN;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[set][j], fa[set][i], acc[i][j], 0, 0, 0);
-      static_for<kPerSlot>([&](auto Q) SHARQ_INLINE { read(int_c<m * kPerSlot + decltype(Q)::value>{}, int_c<set ^ 1>{}, next); });
-      constexpr int lo = (m * C::kLoads + kMfmas - 1) / kMfmas, hi = ((m + 1) * C::kLoads + kMfmas - 1) / kMfmas;
-      static_for<hi - lo>([&](auto Q) SHARQ_INLINE { issue(int_c<lo + decltype(Q)::value>{}); });
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    __builtin_amdgcn_s_setprio(0);
-    cur = next;
-  };
-  int s = 0;
-#pragma unroll 1
-  for (; s + 2 <= steps; s += 2) {
-    body(int_c<0>{});
-    body(int_c<1>{});
-  }
-  if (s < steps) body(int_c<0>{});
-  wait_vmcnt<0>();  // the trailing batches, before the LDS is used again
-
-  if constexpr (C::KS > 1) {
-    ring_barrier();
-    v4i* red = reinterpret_cast<v4i*>(lds);
-    auto place = [&](int i, int q, int j) { return (((wave * C::WM + i) * (C::KS - 1) + q) * C::WN + j) * 64 + lane; };
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i) {
-      const int q = (kg - i % C::KS + C::KS) % C::KS;  // 0: this group finishes row i
-      if (q > 0)
-#pragma unroll
-        for (int j = 0; j < C::WN; ++j) red[place(i, q - 1, j)] = acc[i][j];
-    }
-    ring_barrier();
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i)
-      if (i % C::KS == kg)
-#pragma unroll
-        for (int q = 0; q < C::KS - 1; ++q)
-#pragma unroll
-          for (int j = 0; j < C::WN; ++j) acc[i][j] += red[place(i, q, j)];
-  }
-}
-
-// Eight (kN = 4: four) neighbouring columns to a row of y.
-template <int kN, class Out>
-__device__ __forceinline__ void i8_store(Out* __restrict__ y, const float (&v)[kN], int64_t o, int64_t n, bool wide) {
-  if (wide && o + kN <= n) {
-    if constexpr (sizeof(Out) == 4) {
-#pragma unroll
-      for (int e = 0; e < kN; e += 4)
-        *reinterpret_cast<float4*>(y + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    } else if constexpr (kN == 8) {
-      *reinterpret_cast<uint4*>(y) =
-          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-    } else {
-      *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kN; ++e)
-      if (o + e < n) {
-        if constexpr (sizeof(Out) == 4) y[e] = v[e];
-        else y[e] = (uint16_t)bf16_rne_bits(v[e]);
-      }
-  }
-}
-
-// The sum of a product's codes to its value: the int32 sum rounded once to fp32, a product and a fused one.
-__device__ __forceinline__ float i8_value(int sum, float sa, float sw, float bias) {
-  return fmaf((float)sum * sa, sw, bias);
-}
-
-template <class C, int K>
-__device__ __forceinline__ void i8_epilogue(const v4i (&acc)[C::WM][C::WN], const uint8_t* lds, const TileRows& tr,
-                                            int64_t n0, int64_t n, const I8Out& out) {
-  using Out = std::conditional_t<K == kI8F32, float, uint16_t>;
-  const int lane = threadIdx.x & 63, all = threadIdx.x >> 6;
-  const int kg = all / C::kGroup, wave = all % C::kGroup;
-  const int wm = wave % C::NWM, wn = wave / C::NWM, lr = lane & 15, lc = lane >> 4;
-  const float* sa = reinterpret_cast<const float*>(lds + C::kScaleA);
-  // scales (and biases) of the lane's four weight rows of MFMA tile j
-  auto four = [&](int at, int j) {
-    return *reinterpret_cast<const float4*>(lds + at + 4 * (16 * (C::WN * wn + j) + 4 * lc));
-  };
-#pragma unroll
-  for (int i = 0; i < C::WM; ++i) {
-    if (C::KS > 1 && i % C::KS != kg) continue;  // wave-uniform
-    const int row = 16 * (C::WM * wm + i) + lr;
-    if (row >= tr.rows_valid) continue;
-    const float a = sa[row];
-    Out* y = static_cast<Out*>(out.y) + (tr.m0 + row) * out.ld;
-    if constexpr (K != kI8Silu) {
-#pragma unroll
-      for (int j = 0; j < C::WN; j += 2) {
-        float v[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 w = four(C::kScaleW, j + h), b = four(C::kBias, j + h);
-          v[4 * h] = i8_value(acc[i][j + h][0], a, w.x, b.x);
-          v[4 * h + 1] = i8_value(acc[i][j + h][1], a, w.y, b.y);
-          v[4 * h + 2] = i8_value(acc[i][j + h][2], a, w.z, b.z);
-          v[4 * h + 3] = i8_value(acc[i][j + h][3], a, w.w, b.w);
-        }
-        const int64_t o = n0 + 16 * (C::WN * wn + j) + 8 * lc;
-        i8_store(y + o, v, o, n, out.wide);
-      }
-    } else {
-      constexpr int kPairs = C::WN % 4 == 0 ? 2 : 1;  // gate and up tiles behind a lane's columns
-#pragma unroll
-      for (int j = 0; j < C::WN; j += 2 * kPairs) {
-        float v[4 * kPairs];
-#pragma unroll
-        for (int h = 0; h < kPairs; ++h) {
-          const float4 g = four(C::kScaleW, j + 2 * h), u = four(C::kScaleW, j + 2 * h + 1);
-          const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            v[4 * h + r] = silu_times(i8_value(acc[i][j + 2 * h][r], a, gs[r], 0.0f),
-                                      i8_value(acc[i][j + 2 * h + 1][r], a, us[r], 0.0f));
-        }
-        const int64_t o = n0 + 8 * (C::WN * wn + j) + 4 * kPairs * lc;
-        i8_store(y + o, v, o, n, out.wide);
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ TileRows i8_dense_rows(int64_t m0, int64_t T, int bm) {
-  TileRows tr;
-  tr.m0 = m0;
-  tr.rows_valid = T - m0 < bm ? T - m0 : bm;
-  tr.gather = nullptr;
-  tr.src_rows = T;
-  return tr;
-}
-
-template <class C, int K>
-__device__ __forceinline__ void i8_tile(const I8Operands& op, const TileRows& tr, int64_t n0, const I8Out& out,
-                                        uint8_t* lds) {
-  constexpr bool kSilu = K == kI8Silu;
-  const int64_t n = kSilu ? out.I : op.O;
-  v4i acc[C::WM][C::WN];
-  i8_mainloop<C, kSilu>(op, tr, I8Cols<C, kSilu>{n0, n}, lds, acc);
-  i8_epilogue<C, K>(acc, lds, tr, n0, n, out);
-}
 
 template <class C, int K>
 __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_linear_kernel(I8Operands op, I8Out out,
@@ -374,146 +14,6 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_linear_kerne
   i8_tile<C, K>(op, i8_dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM), (int64_t)ti.tn * kI8Cols<C, K>, out, lds);
 }
 
-__device__ __forceinline__ void i8_select_expert(I8Operands& op, int e) {
-  op.w_codes += (int64_t)e * op.O * kRowBytes * op.nsteps;
-  op.w_scales += (int64_t)e * op.O;
-}
-
-template <class C, int K>
-__global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_grouped_kernel(
-    I8Operands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, int64_t P, I8Out out,
-    int tiles_n) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
-  const GroupedTile g = grouped_tile<C, true>(seg, E, P, a_rows, op.rows, tiles_n);
-  if (g.e < 0) return;  // uniform across the workgroup
-  i8_select_expert(op, g.e);
-  i8_tile<C, K>(op, g.tr, (int64_t)g.col * kI8Cols<C, K>, out, lds);
-}
-
-// ---------------------------------------------------------------------------
-// Few rows: operands straight into registers
-// ---------------------------------------------------------------------------
-
-// BM = 16 WM tokens x BN = 16 WN weight rows; the KW waves of a workgroup divide
-// K, stage s to wave s % KW, and add their sums through LDS at the end. No
-// operand passes through LDS and no barrier stands in the loop: a wave keeps the
-// loads of PF stages in flight, which is what streaming a weight at the rate of
-// memory takes.
-template <int WM_, int WN_, int KW_, int PF_>
-struct I8Thin {
-  static constexpr int WM = WM_, WN = WN_, KW = KW_, PF = PF_;
-  static constexpr int BM = 16 * WM, BN = 16 * WN, kThreads = 64 * KW;
-  static constexpr int kLds = KW * WM * WN * 1024;
-  static_assert(kLds <= kLdsBytes - 64, "the waves' sums");
-};
-using I8Thin16 = I8Thin<1, 2, 16, 4>;
-using I8Thin32 = I8Thin<2, 2, 16, 4>;
-
-template <class C, int K>
-__device__ __forceinline__ void i8_thin_tile(const I8Operands& op, const TileRows& tr, int64_t n0, const I8Out& out,
-                                             uint8_t* lds) {
-  constexpr bool kSilu = K == kI8Silu;
-  using Out = std::conditional_t<K == kI8F32, float, uint16_t>;
-  const int64_t n = kSilu ? out.I : op.O;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 15, lc = lane >> 4;
-  // MFMA tile j has columns n0 + 16 j on; gate|up: gate (j even) or up (j odd) of h columns n0 + 16 (j / 2) on
-  auto w_row = [&](int j, int r) -> int64_t {
-    const int64_t o = n0 + 16 * (kSilu ? j / 2 : j) + r;
-    return o < n ? o + (kSilu && (j & 1) ? n : 0) : -1;
-  };
-  uint32_t a_off[C::WM], w_off[C::WN];
-#pragma unroll
-  for (int i = 0; i < C::WM; ++i) {
-    const int64_t src = tr.src(16 * i + lr);
-    a_off[i] = src >= 0 ? (uint32_t)(src * kRowBytes + 16 * lc) : kOOB;
-  }
-#pragma unroll
-  for (int j = 0; j < C::WN; ++j) {
-    const int64_t src = w_row(j, lr);
-    w_off[j] = src >= 0 ? (uint32_t)(src * kRowBytes + 16 * lc) : kOOB;
-  }
-  const int64_t a_stage = op.rows * kRowBytes, w_stage = op.O * kRowBytes;
-  const int8_t *a = op.a_codes + wave * a_stage, *w = op.w_codes + wave * w_stage;
-  int left = (op.nsteps - wave + C::KW - 1) / C::KW;  // stages of this wave not yet asked for
-  const int trips = left;
-  v4i fa[C::PF][C::WM], fw[C::PF][C::WN];
-  auto load = [&](auto U) SHARQ_INLINE {  // past the last stage: views of nothing
-    constexpr int u = decltype(U)::value;
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)a, 0, left > 0 ? (int)a_stage : 0, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)w, 0, left > 0 ? (int)w_stage : 0, 0x00020000);
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j) fw[u][j] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_off[j], 0, 0);
-#pragma unroll
-    for (int i = 0; i < C::WM; ++i) fa[u][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off[i], 0, 0);
-    a += C::KW * a_stage;
-    w += C::KW * w_stage;
-    --left;
-  };
-  static_for<C::PF>(load);
-  // the scales of the columns that the thread finishes
-  const int unit = threadIdx.x;
-  constexpr int kCols = kSilu ? C::WN / 2 : C::WN, kUnits = 64 * C::WM * kCols;
-  static_assert(kUnits <= C::kThreads, "a thread finishes four columns at most");
-  const int ui = unit >> 6 < C::WM * kCols ? (unit >> 6) / kCols : 0, uj = (unit >> 6) % kCols;
-  float sa = 0.0f, sw[4], su[4], bias[4];
-  if (unit < kUnits) {
-    const int64_t src = tr.src(16 * ui + lr);
-    if (src >= 0) sa = op.a_scales[src];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t o = w_row(kSilu ? 2 * uj : uj, 4 * lc + r);
-      sw[r] = o >= 0 ? op.w_scales[o] : 0.0f;
-      bias[r] = o >= 0 && op.bias ? op.bias[o] : 0.0f;
-      su[r] = kSilu && o >= 0 ? op.w_scales[o + n] : 0.0f;
-    }
-  }
-  v4i acc[C::WM][C::WN];
-#pragma unroll
-  for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j) acc[i][j] = v4i{};
-#pragma unroll 1
-  for (int s = 0; s < trips; s += C::PF)
-    static_for<C::PF>([&](auto U) SHARQ_INLINE {
-      constexpr int u = decltype(U)::value;
-#pragma unroll
-      for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::WN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][j], fa[u][i], acc[i][j], 0, 0, 0);
-      load(U);
-    });
-
-  v4i* red = reinterpret_cast<v4i*>(lds);
-#pragma unroll
-  for (int i = 0; i < C::WM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::WN; ++j) red[((wave * C::WM + i) * C::WN + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  if (unit >= kUnits) return;
-  auto sum = [&](int j) {
-    v4i v = v4i{};
-#pragma unroll
-    for (int q = 0; q < C::KW; ++q) v += red[((q * C::WM + ui) * C::WN + j) * 64 + lane];
-    return v;
-  };
-  float v[4];
-  if constexpr (kSilu) {
-    const v4i g = sum(2 * uj), u = sum(2 * uj + 1);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = silu_times(i8_value(g[r], sa, sw[r], 0.0f), i8_value(u[r], sa, su[r], 0.0f));
-  } else {
-    const v4i q = sum(uj);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = i8_value(q[r], sa, sw[r], bias[r]);
-  }
-  const int row = 16 * ui + lr;
-  if (row >= tr.rows_valid) return;
-  const int64_t o = n0 + 16 * uj + 4 * lc;
-  i8_store(static_cast<Out*>(out.y) + (tr.m0 + row) * out.ld + o, v, o, n, out.wide);
-}
-
 template <class C, int K>
 __global__ __launch_bounds__(C::kThreads) void i8_thin_kernel(I8Operands op, I8Out out, int tiles_m) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
@@ -521,93 +21,53 @@ __global__ __launch_bounds__(C::kThreads) void i8_thin_kernel(I8Operands op, I8O
   i8_thin_tile<C, K>(op, i8_dense_rows((int64_t)tm * C::BM, op.rows, C::BM), (int64_t)tn * kI8Cols<C, K>, out, lds);
 }
 
-template <class C, int K>
-__global__ __launch_bounds__(C::kThreads) void i8_thin_grouped_kernel(I8Operands op, const int32_t* __restrict__ a_rows,
-                                                                      const int32_t* __restrict__ seg, int E,
-                                                                      int64_t P, I8Out out, int tiles_n) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
-  const GroupedTile g = grouped_tile<C, false>(seg, E, P, a_rows, op.rows, tiles_n);
-  if (g.e < 0) return;  // uniform across the workgroup
-  i8_select_expert(op, g.e);
-  i8_thin_tile<C, K>(op, g.tr, (int64_t)g.col * kI8Cols<C, K>, out, lds);
-}
+constexpr int kI8Tiles = 12;
+constexpr I8TileCost kI8Costs[kI8Tiles] = {
+    {16, 32, 0.012, 0.040, 0.68, 2.6},   {32, 32, 0.051, 0.070, 0.57, 2.5},   {64, 32, 0.101, 0.067, 1.22, 3.2},
+    {64, 64, 0.056, 0.104, 1.18, 2.6},   {64, 128, 0.045, 0.180, 0.43, 2.2},  {64, 128, 0.055, 0.152, 0.98, 2.6},
+    {128, 128, 0.139, 0.230, 1.6, 3.0},  {128, 128, 0.125, 0.218, 1.18, 3.8}, {128, 256, 0.092, 0.477, 1.32, 2.75},
+    {256, 128, 0.106, 0.387, 1.16, 3.6}, {256, 128, 0.087, 0.325, 10.0, 0.0}, {256, 256, 0.110, 0.670, 2.7, 3.6}};
 
-// ---------------------------------------------------------------------------
-// Launch
-// ---------------------------------------------------------------------------
-
-I8Operands i8_operands(const I8Product& p) {
-  return I8Operands{p.a_codes, p.a_scales, p.w_codes, p.w_scales, p.bias, p.rows, p.O, (int)((p.K + 63) / 64)};
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct I8TileCost {
-  int64_t rows, cols;
-  double alone, each;  // microseconds a stage of a workgroup on a CU of its own, and of each of several
-};
-constexpr int kI8Tiles = 9;
-constexpr I8TileCost kCosts[kI8Tiles] = {
-    {16, 32, 0.05, 0.05},    {32, 32, 0.05, 0.06},   {64, 64, 0.06, 0.06},    {64, 128, 0.10, 0.10},
-    {128, 128, 0.14, 0.14}, {128, 128, 0.25, 0.22}, {128, 256, 0.26, 0.24}, {128, 256, 0.45, 0.43}, {256, 256, 0.85, 0.85}};
-
-// Calls f with the tile type of kCosts[tile].
+// Calls f with the tile type of kI8Costs[tile] and whether it is a thin one.
 template <class F>
 void i8_with_tile(int tile, F f) {
   switch (tile) {
     case 0: f(I8Thin16{}, std::true_type{}); break;
     case 1: f(I8Thin32{}, std::true_type{}); break;
-    case 2: f(I8x64x64k4{}, std::false_type{}); break;
-    case 3: f(I8x64x128k2{}, std::false_type{}); break;
-    case 4: f(I8x128x128k2{}, std::false_type{}); break;
-    case 5: f(I8x128x128{}, std::false_type{}); break;
-    case 6: f(I8x128x256k2{}, std::false_type{}); break;
-    case 7: f(I8x128x256{}, std::false_type{}); break;
+    case 2: f(I8Thin64{}, std::true_type{}); break;
+    case 3: f(I8x64x64k4{}, std::false_type{}); break;
+    case 4: f(I8x64x128{}, std::false_type{}); break;
+    case 5: f(I8x64x128k2{}, std::false_type{}); break;
+    case 6: f(I8x128x128{}, std::false_type{}); break;
+    case 7: f(I8x128x128k2{}, std::false_type{}); break;
+    case 8: f(I8x128x256{}, std::false_type{}); break;
+    case 9: f(I8x256x128{}, std::false_type{}); break;
+    case 10: f(I8x256x128k2{}, std::false_type{}); break;
     default: f(I8x256x256{}, std::false_type{}); break;
   }
 }
 
-int64_t i8_cols(int64_t O, bool silu, int tile) {
-  return silu ? ceil_div(O / 2, kCosts[tile].cols / 2) : ceil_div(O, kCosts[tile].cols);
+// The cheapest tile by the costs, which are fitted to timed launches of all of them
+// on 10 layer shapes from 512 x 4096 to 4096 x 28672 (K x O), T = 1 .. 4096, and
+// the 8192 x 57344 pair: within 1.3% of the best on average, 15% at most.
+int i8_dense_tile(int64_t T, int64_t O, int64_t K, I8Kind kind) {
+  const double bytes = ((double)O + (double)T) * (double)K + i8_out_bytes(T, O, kind);
+  int pick = kI8Tiles - 1;
+  double best = 0;
+  for (int t = kI8Tiles - 1; t >= 0; --t) {
+    const int64_t tiles = ceil_div(T, kI8Costs[t].rows) * i8_cols(O, kind == kI8Silu, kI8Costs[t]);
+    if (tiles >= kI8MaxWorkgroups) break;  // narrower ones are more
+    const double us = i8_cost(kI8Costs[t], (double)ceil_div(tiles, 256), ceil_div(K, 64), bytes);
+    if (t == kI8Tiles - 1 || us < best) best = us, pick = t;
+  }
+  return pick;
 }
 
-// Tile of a dense product.
-int i8_dense_tile(int64_t T, int64_t O, int64_t K, bool silu) {
-  (void)K;
-  (void)silu;
-  const int64_t big = ceil_div(T, 128) * ceil_div(O, 256);
-  if (T <= 16) return 0;
-  if (T <= 32) return 1;
-  if (big >= 1024) return 8;
-  if (big >= 400) return 7;
-  if (big >= 160) return 6;
-  if (ceil_div(T, 128) * ceil_div(O, 128) >= 160) return 4;
-  return ceil_div(T, 64) * ceil_div(O, 128) >= 160 ? 3 : 2;
-}
-
-// Row slots of a grouped launch: no sorted segments of P rows fill more tiles.
-int64_t i8_row_slots(int64_t P, int64_t E, int tile) {
-  const int64_t filled = P < E ? P : E;
-  return filled + (P - filled) / kCosts[tile].rows;
-}
-
-int i8_grouped_tile(int64_t P, int64_t E, int64_t O, int64_t K, bool silu) {
-  (void)K;
-  (void)silu;
-  const int64_t filled = P < E ? P : E, mean = P / filled;
-  if (mean <= 12) return 0;
-  if (mean <= 24) return 1;
-  if (mean <= 64) return 3;
-  return filled * ceil_div(mean, 128) * ceil_div(O, 256) >= 400 ? 7 : 5;
-}
-
-bool i8_wide(const void* y, int64_t ld, int64_t bytes) {
-  return (reinterpret_cast<uintptr_t>(y) & 15) == 0 && ld * bytes % 16 == 0;
-}
-
-template <int K>
-hipError_t i8_launch_dense(const I8Operands& op, const I8Out& out, int tile, hipStream_t stream) {
-  const int64_t tiles_m = ceil_div(op.rows, kCosts[tile].rows), tiles = tiles_m * i8_cols(op.O, K == kI8Silu, tile);
+template <I8Kind K>
+hipError_t i8_launch_dense(const I8Operands& op, const I8Out& out, int64_t K_, hipStream_t stream) {
+  const int tile = i8_dense_tile(op.rows, op.O, K_, K);
+  const int64_t tiles_m = ceil_div(op.rows, kI8Costs[tile].rows),
+                tiles = tiles_m * i8_cols(op.O, K == kI8Silu, kI8Costs[tile]);
   i8_with_tile(tile, [&](auto c, auto thin) {
     using C = decltype(c);
     if constexpr (decltype(thin)::value)
@@ -620,69 +80,25 @@ hipError_t i8_launch_dense(const I8Operands& op, const I8Out& out, int tile, hip
   return hipGetLastError();
 }
 
-template <int K>
-hipError_t i8_launch_grouped(const I8Operands& op, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
-                             const I8Out& out, int tile, hipStream_t stream) {
-  const int64_t tiles_n = i8_cols(op.O, K == kI8Silu, tile);
-  const dim3 grid((unsigned)((i8_row_slots(P, E, tile) * tiles_n + 7) / 8 * 8));  // XCDs take equal shares
-  i8_with_tile(tile, [&](auto c, auto thin) {
-    using C = decltype(c);
-    if constexpr (decltype(thin)::value)
-      hipLaunchKernelGGL((i8_thin_grouped_kernel<C, K>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, P, out,
-                         (int)tiles_n);
-    else
-      hipLaunchKernelGGL((i8_grouped_kernel<C, K>), grid, dim3(C::kThreads), 0, stream, op, a_rows, seg, E, P, out,
-                         (int)tiles_n);
-  });
-  return hipGetLastError();
-}
-
-int64_t i8_h_ld(int64_t I) { return (I + 7) & ~(int64_t)7; }
-
 }  // namespace
 
-bool i8_linear_fits(int64_t T, int64_t O) { return ceil_div(T, 64) * ceil_div(O, 64) < kI8MaxWorkgroups; }
+bool i8_linear_fits(int64_t T, int64_t O) { return ceil_div(T, 256) * ceil_div(O, 256) < kI8MaxWorkgroups; }
 
 hipError_t launch_i8_linear(const I8Product& p, void* y, int64_t ldy, bool bf16, hipStream_t stream) {
   const I8Operands op = i8_operands(p);
   const I8Out out{y, ldy, i8_wide(y, ldy, bf16 ? 2 : 4), 0};
-  const int tile = i8_dense_tile(p.rows, p.O, p.K, false);
-  return bf16 ? i8_launch_dense<kI8Bf16>(op, out, tile, stream) : i8_launch_dense<kI8F32>(op, out, tile, stream);
+  return bf16 ? i8_launch_dense<kI8Bf16>(op, out, p.K, stream) : i8_launch_dense<kI8F32>(op, out, p.K, stream);
 }
 
 int64_t i8_silu_workspace_bytes(int64_t T, int64_t I) { return T * i8_h_ld(I) * 2; }
 
 hipError_t launch_i8_linear_silu(const I8Product& p, int8_t* h_codes, float* h_scales, void* workspace,
                                  hipStream_t stream) {
-  const I8Operands op = i8_operands(p);
   const int64_t I = p.O / 2, ld = i8_h_ld(I);
   const I8Out out{workspace, ld, true, I};
-  const hipError_t e = i8_launch_dense<kI8Silu>(op, out, i8_dense_tile(p.rows, p.O, p.K, true), stream);
+  const hipError_t e = i8_launch_dense<kI8Silu>(i8_operands(p), out, p.K, stream);
   if (e != hipSuccess) return e;
   return launch_quantize_int8(workspace, 1, 1, p.rows, I, ld, h_codes, h_scales, nullptr, 0, stream);
-}
-
-bool i8_grouped_fits(int64_t P, int32_t E, int64_t O) {
-  return (i8_row_slots(P, E, 0) + 1) * (ceil_div(O, 32) + 1) < kI8MaxWorkgroups;
-}
-
-hipError_t launch_i8_grouped(const I8Product& p, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
-                             void* y, bool bf16, hipStream_t stream) {
-  const I8Operands op = i8_operands(p);
-  const I8Out out{y, p.O, i8_wide(y, p.O, bf16 ? 2 : 4), 0};
-  const int tile = i8_grouped_tile(P, E, p.O, p.K, false);
-  return bf16 ? i8_launch_grouped<kI8Bf16>(op, a_rows, seg, E, P, out, tile, stream)
-              : i8_launch_grouped<kI8F32>(op, a_rows, seg, E, P, out, tile, stream);
-}
-
-hipError_t launch_i8_grouped_silu(const I8Product& p, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
-                                  int8_t* h_codes, float* h_scales, void* workspace, hipStream_t stream) {
-  const I8Operands op = i8_operands(p);
-  const int64_t I = p.O / 2, ld = i8_h_ld(I);
-  const I8Out out{workspace, ld, true, I};
-  const hipError_t e = i8_launch_grouped<kI8Silu>(op, a_rows, seg, E, P, out, i8_grouped_tile(P, E, p.O, p.K, true), stream);
-  if (e != hipSuccess) return e;
-  return launch_quantize_int8(workspace, 1, 1, P, I, ld, h_codes, h_scales, seg, E, stream);
 }
 
 }  // namespace sharq

@@ -4,16 +4,18 @@
 //   amax = max_k |x'[k]|,  s = fp32(amax / 127),  q[k] = clamp(rne(x'[k] / s), -127, 127)
 //
 // with x' = x, or the RMS-normed row bf16(x r) gamma. The quotient is the exact
-// one, not its fp32 rounding: v = x' (1 / s) is at most 127 (2^-23 + 2^-47) <
-// 2^-16 from it, so wherever v stays 2^-15 off the middle of two codes its
-// nearest integer is the code; a thread that holds a closer one settles its
-// entries by the sign of |x' - q s| - s / 2, where x' - q s is one fma, exact
-// that near the middle (a multiple of the last bit of s below s). Rows of zeros
-// have scale 0; a row that holds a NaN or an infinity has scale NaN and codes
-// of zero, so that products with it are NaN.
+// one, not its fp32 rounding. t = fma(x', 1 / s, 1.5 2^23) holds the integer nearest
+// to x' (1 / s), which is at most 127 2^-24 off the quotient, so that q is the code
+// or its neighbour. The rest x' - q s is one fma, exact (a multiple of the last bit
+// of s or of x' below s), so q is the code wherever |rest| < s / 2; a thread that
+// holds another entry settles its piece by the rest's sign. Rows of zeros have scale
+// 0; a row that holds a NaN or an infinity has scale NaN and codes of zero, so that
+// products with it are NaN.
 //
 // Layout: codes i8 [G][rows][64], G = ceil(K / 64), zeros past K: a stage of 64
 // entries a row is the 64-byte row that the GEMM's LDS stage holds.
+
+#include <type_traits>
 
 #include "gemm_common.h"
 #include "sharq_device.h"
@@ -22,47 +24,51 @@
 namespace sharq {
 namespace {
 
-constexpr int kPiece = 8;  // entries of a lane's load
+constexpr int kPiece = 16;  // entries that a lane codes together: 16 bytes of codes
 
-// The entries of a piece as they were loaded: 16 bytes of a 2-byte type, 32 of fp32.
+// The entries of a piece as they were loaded: two to a dword, or fp32.
 template <class In>
 struct Piece {
-  uint32_t w[sizeof(In) * kPiece / 4];
+  static constexpr int kWords = sizeof(In) * kPiece / 4;
+  uint32_t w[kWords];
 };
 
 __device__ __forceinline__ void widen(const Piece<uint16_t>& p, float (&v)[kPiece]) {  // bf16
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(p.w[i]), v[2 * i + 1] = bf16_hi(p.w[i]);
+  for (int i = 0; i < kPiece / 2; ++i) v[2 * i] = bf16_lo(p.w[i]), v[2 * i + 1] = bf16_hi(p.w[i]);
 }
 __device__ __forceinline__ void widen(const Piece<_Float16>& p, float (&v)[kPiece]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPiece / 2; ++i) {
     v[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)p.w[i]);
     v[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(p.w[i] >> 16));
   }
 }
 __device__ __forceinline__ void widen(const Piece<float>& p, float (&v)[kPiece]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(p.w[i]);
+  for (int i = 0; i < kPiece; ++i) v[i] = __uint_as_float(p.w[i]);
 }
 
-// Entries [8 p, 8 p + 8) of a row of K; those past K are zeros. kWide: K is a
+// Entries [16 p, 16 p + 16) of a row of K; those past K are zeros. kWide: K is a
 // multiple of 8 and the row 16-byte aligned.
 template <class In, bool kWide>
 __device__ __forceinline__ Piece<In> load_piece(const In* __restrict__ row, uint32_t p, uint32_t K) {
   Piece<In> out;
-  constexpr int kWords = sizeof(Piece<In>) / 4;
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) out.w[i] = 0;
+  for (int i = 0; i < Piece<In>::kWords; ++i) out.w[i] = 0;
   if constexpr (kWide) {
-    if (kPiece * p < K) {
-      const uint4* src = reinterpret_cast<const uint4*>(row + (uint64_t)kPiece * p);
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = src[i];
-        out.w[4 * i] = v.x, out.w[4 * i + 1] = v.y, out.w[4 * i + 2] = v.z, out.w[4 * i + 3] = v.w;
+    for (int h = 0; h < 2; ++h)
+      if (kPiece * p + 8 * h < K) {
+        constexpr int kHalf = Piece<In>::kWords / 2;
+        const uint4* src = reinterpret_cast<const uint4*>(row + (uint64_t)kPiece * p + 8 * h);
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i) {
+          const uint4 v = src[i];
+          uint32_t* w = out.w + kHalf * h + 4 * i;
+          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
       }
-    }
   } else {
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) {
@@ -76,19 +82,69 @@ __device__ __forceinline__ Piece<In> load_piece(const In* __restrict__ row, uint
   return out;
 }
 
-// x' of a normed piece from its bf16 entries (x r, rounded) and gamma (exact in fp32).
-__device__ __forceinline__ void times_gamma(float (&v)[kPiece], const Piece<uint16_t>& gamma) {
-  float g[kPiece];
-  widen(gamma, g);
+// Largest magnitude of a piece as a bit pattern of its type (NaN above infinity
+// above all numbers), joined to m: two 16-bit patterns in a dword, or fp32's.
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+template <class In>
+__device__ __forceinline__ uint32_t join_amax(uint32_t m, const Piece<In>& p) {
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) v[i] *= g[i];
+  for (int i = 0; i < Piece<In>::kWords; ++i) {
+    if constexpr (sizeof(In) == 4)
+      m = max(m, p.w[i] & 0x7FFFFFFFu);
+    else
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2us, m),
+                                                                 __builtin_bit_cast(v2us, p.w[i] & 0x7FFF7FFFu)));
+  }
+  return m;
+}
+// The fp32 bits of the magnitude that join_amax found.
+template <class In>
+__device__ __forceinline__ uint32_t amax_f32(uint32_t m) {
+  if constexpr (sizeof(In) == 4) return m;
+  const uint32_t h = max(m & 0xFFFFu, m >> 16);
+  if constexpr (std::is_same<In, uint16_t>::value) return h << 16;
+  else return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)h));
+}
+
+// Over the wave, in all lanes: rotations within the rows of 16 lanes, then the four rows' values.
+template <int kBy>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + kBy, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, row_ror<8>(v));
+  v = max(v, row_ror<4>(v));
+  v = max(v, row_ror<2>(v));
+  v = max(v, row_ror<1>(v));
+  uint32_t m = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) m = max(m, (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * r));
+  return m;
+}
+template <int kBy>
+__device__ __forceinline__ double row_ror_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)row_ror<kBy>((uint32_t)(b >> 32)) << 32 | row_ror<kBy>((uint32_t)b));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += row_ror_f64<8>(v);
+  v += row_ror_f64<4>(v);
+  v += row_ror_f64<2>(v);
+  v += row_ror_f64<1>(v);
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  double s = 0.0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    s += __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 16 * r) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 16 * r));
+  return s;
 }
 
 // How a row is divided: x' up (1 / (s up)), up a power of two that keeps the
 // reciprocal of a small scale finite.
 struct Divisor {
   float up, scale, inverse;  // scale: s up
-  bool tiny;                 // s has lost bits of amax / 127, so codes may pass 127
+  bool tiny;                 // s may have lost bits of amax / 127, so that codes pass 127
 };
 
 __device__ __forceinline__ Divisor divisor(float s) {
@@ -100,45 +156,46 @@ __device__ __forceinline__ Divisor divisor(float s) {
   return d;
 }
 
-// Eight codes, a byte each. x + 1.5 2^23 rounds x to the nearest integer, ties
+// Sixteen codes, a byte each. x + 1.5 2^23 rounds x to the nearest integer, ties
 // to even, and holds it in its low bits in two's complement.
-__device__ __forceinline__ uint2 code_piece(float (&x)[kPiece], const Divisor& d) {
+__device__ __forceinline__ uint4 code_piece(float (&x)[kPiece], const Divisor& d) {
   constexpr float kMagic = 0x1.8p23f;
+  const float half = 0.5f * d.scale;
   float off = 0.0f, t[kPiece];
-  if (d.tiny) {
+  if (d.tiny) {  // uniform over the row
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) x[i] = fminf(fmaxf(x[i] * d.up, -127.0f * d.scale), 127.0f * d.scale);
   }
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) {
-    const float v = x[i] * d.inverse;
-    t[i] = v + kMagic;
-    off = fmaxf(off, fabsf(v - (t[i] - kMagic)));
+    t[i] = fmaf(x[i], d.inverse, kMagic);
+    off = fmaxf(off, fabsf(fmaf(kMagic - t[i], d.scale, x[i])));
   }
-  if (off > 0.5f - 0x1p-15f) {
-    const float half = 0.5f * d.scale;
+  if (off >= half && half > 0.0f) {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      const float q = t[i] - kMagic, rest = fmaf(-q, d.scale, x[i]);
+      const float rest = fmaf(kMagic - t[i], d.scale, x[i]);
       const bool over = fabsf(rest) > half || (fabsf(rest) == half && (__float_as_uint(t[i]) & 1u));
-      if (over && d.inverse > 0.0f) t[i] += rest > 0.0f ? 1.0f : -1.0f;
+      if (over) t[i] += rest > 0.0f ? 1.0f : -1.0f;
     }
   }
-  uint32_t w[2];
+  uint32_t w[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 4; ++h) {
     const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 1]), __float_as_uint(t[4 * h]), 0x0C0C0400u);
     const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 3]), __float_as_uint(t[4 * h + 2]), 0x04000C0Cu);
     w[h] = lo | hi;
   }
-  return make_uint2(w[0], w[1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[kPiece]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < kPiece; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+// fp32(1 / sqrt(v)), v > 0: the hardware's estimate y of 2^-23, and the third-order
+// step y (1 + e / 2 + 3 e^2 / 8), e = 1 - v y^2, after which a few roundings of
+// 2^-53 are left (with a division and a square root of float64 the normed 2048 x
+// 4096 take 10.7 us, 10.1 so). Not finite where v is not.
+__device__ __forceinline__ float inverse_root(double v) {
+  const double y = __builtin_amdgcn_rsq(v), e = fma(-(v * y), y, 1.0);
+  return (float)fma(y, e * fma(0.375, e, 0.5), y);
 }
 
 struct QuantArgs {
@@ -146,6 +203,7 @@ struct QuantArgs {
   int64_t ldx;
   const uint16_t* gamma;  // norm: bf16 [K] or null
   float eps;
+  double inverse_k;
   float* r_out;  // norm: fp32 [rows] or null
   uint32_t K, rows;
   uint32_t per;  // rows of a tensor (a stack holds rows / per of them)
@@ -157,8 +215,9 @@ struct QuantArgs {
 
 // A workgroup has a row, a lane the pieces tid, tid + threads, ..., of which the
 // first kHold stay in registers between the passes over the row (a sum for the
-// norm, the maximum, the codes); later ones are read again. Bound by memory at
-// many rows (3 bytes an entry), by the round trips of one row at few.
+// norm, the maximum, the codes); later ones are read again. Many rows: bound by
+// memory where rows are long, by the instructions where they are short (an entry
+// takes about 8 of them, with the norm 16). Few: by one row's round trips.
 template <class In, bool kNorm, bool kWide, int kHold>
 __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
   __shared__ double s_sum[16];
@@ -172,7 +231,7 @@ __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
     if ((int64_t)t < lo || (int64_t)t >= hi) return;
   }
   const In* row = static_cast<const In*>(a.x) + (int64_t)t * a.ldx;
-  const uint32_t pieces = (a.K + kPiece - 1) / kPiece, stages = (a.K + 63) / 64, padded = 8 * stages;
+  const uint32_t pieces = (a.K + kPiece - 1) / kPiece, stages = (a.K + 63) / 64, padded = 4 * stages;
   Piece<In> held[kHold];
   Piece<uint16_t> gam[kNorm ? kHold : 1];
 #pragma unroll
@@ -185,29 +244,28 @@ __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
 
   float r = 0.0f;
   if constexpr (kNorm) {
-    // Squares of bf16 are exact in fp32; their sum is float64, in an order set by K alone.
+    // Sums of squares in float64 (each square exact), in an order set by the sizes alone.
     double sum = 0.0;
     auto add = [&](const Piece<In>& p) {
       float v[kPiece];
       widen(p, v);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) sum += (double)(v[i] * v[i]);
+      for (int i = 0; i < kPiece; ++i) sum = fma((double)v[i], (double)v[i], sum);
     };
 #pragma unroll
     for (int q = 0; q < kHold; ++q) add(held[q]);
     for (uint32_t p = tid + kHold * blockDim.x; p < pieces; p += blockDim.x) add(load_piece<In, kWide>(row, p, a.K));
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    sum = wave_sum(sum);
     if (waves > 1) {
       if (lane == 0) s_sum[wave] = sum;
       __syncthreads();
       sum = 0.0;
       for (uint32_t i = 0; i < waves; ++i) sum += s_sum[i];
     }
-    r = (float)(1.0 / sqrt(sum / (double)a.K + (double)a.eps));
+    r = inverse_root(fma(sum, a.inverse_k, (double)a.eps));
     if (a.r_out && tid == 0) a.r_out[t] = r;
   }
-  auto values = [&](const Piece<In>& p, const Piece<uint16_t>& g, float (&v)[kPiece]) {
+  auto norm = [&](const Piece<In>& p, const Piece<uint16_t>& gamma, float (&v)[kPiece]) {
     widen(p, v);
     if constexpr (kNorm) {
 #pragma unroll
@@ -216,30 +274,48 @@ __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
         v[i] = bf16_lo(b);
         v[i + 1] = bf16_hi(b);
       }
-      if (a.gamma) times_gamma(v, g);
+      if (a.gamma) {
+        float g[kPiece];
+        widen(gamma, g);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) v[i] *= g[i];
+      }
     }
   };
   auto later = [&](uint32_t p, float (&v)[kPiece]) {
     Piece<uint16_t> g;
     if constexpr (kNorm)
       if (a.gamma) g = load_piece<uint16_t, kWide>(a.gamma, p, a.K);
-    values(load_piece<In, kWide>(row, p, a.K), g, v);
+    norm(load_piece<In, kWide>(row, p, a.K), g, v);
+  };
+  auto largest = [&](uint32_t m, const float (&v)[kPiece]) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
   };
 
+  // A normed row's held entries stay as their fp32 values, a plain row's as they were loaded.
+  float value[kNorm ? kHold : 1][kPiece];
   uint32_t m = 0;
+  if constexpr (kNorm) {
 #pragma unroll
-  for (int q = 0; q < kHold; ++q) {
-    float v[kPiece];
-    values(held[q], gam[kNorm ? q : 0], v);
-    m = max(m, amax_bits(v));
-  }
-  for (uint32_t p = tid + kHold * blockDim.x; p < pieces; p += blockDim.x) {
-    float v[kPiece];
-    later(p, v);
-    m = max(m, amax_bits(v));
-  }
+    for (int q = 0; q < kHold; ++q) {
+      norm(held[q], gam[q], value[q]);
+      m = largest(m, value[q]);
+    }
+    for (uint32_t p = tid + kHold * blockDim.x; p < pieces; p += blockDim.x) {
+      float v[kPiece];
+      later(p, v);
+      m = largest(m, v);
+    }
+  } else {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    for (int q = 0; q < kHold; ++q) m = join_amax<In>(m, held[q]);
+    for (uint32_t p = tid + kHold * blockDim.x; p < pieces; p += blockDim.x)
+      m = join_amax<In>(m, load_piece<In, kWide>(row, p, a.K));
+    m = amax_f32<In>(m);
+  }
+  m = wave_max(m);
   if (waves > 1) {
     if (lane == 0) s_max[wave] = m;
     __syncthreads();
@@ -251,24 +327,26 @@ __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
   if (tid == 0) a.scales[t] = s;
 
   const uint32_t tensor = t / a.per, at = t - tensor * a.per;
-  int8_t* out = a.codes + ((int64_t)tensor * stages * a.per + at) * 64;
-  auto emit = [&](uint32_t p, float (&v)[kPiece]) {
-    const uint2 c = finite ? code_piece(v, d) : make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(out + (int64_t)(p >> 3) * a.per * 64 + 8 * (p & 7)) = c;
-  };
+  const int64_t stage = (int64_t)a.per * 64;
+  int8_t* out = a.codes + (int64_t)tensor * stages * stage + (int64_t)at * 64 + (tid >> 2) * stage + 16 * (tid & 3);
+  const int64_t step = (blockDim.x >> 2) * stage;
 #pragma unroll
   for (int q = 0; q < kHold; ++q) {
-    const uint32_t p = tid + q * blockDim.x;
-    if (p < padded) {
-      float v[kPiece];
-      values(held[q], gam[kNorm ? q : 0], v);
-      emit(p, v);
+    if (tid + q * blockDim.x < padded) {
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (finite) {
+        float v[kPiece];
+        if constexpr (!kNorm) widen(held[q], v);
+        c = code_piece(kNorm ? value[kNorm ? q : 0] : v, d);
+      }
+      *reinterpret_cast<uint4*>(out + q * step) = c;
     }
   }
-  for (uint32_t p = tid + kHold * blockDim.x; p < padded; p += blockDim.x) {
+  out += kHold * step;
+  for (uint32_t p = tid + kHold * blockDim.x; p < padded; p += blockDim.x, out += step) {
     float v[kPiece];
     later(p, v);
-    emit(p, v);
+    *reinterpret_cast<uint4*>(out) = finite ? code_piece(v, d) : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -329,23 +407,22 @@ dim3 rows_grid(int64_t n) {
 template <class In, bool kNorm>
 hipError_t launch_rows(const QuantArgs& a, hipStream_t stream) {
   const int64_t pieces = (a.K + kPiece - 1) / kPiece;
-  // Many rows: few waves a row, whose lanes hold four pieces (with gamma's) or
-  // eight. Few: two a lane, for the row's own latency counts.
-  constexpr int kMost = kNorm ? 4 : 8;
-  const int64_t each = a.rows >= 1024 ? kMost : 2;
+  // A piece a lane, which has most in flight: 2048 x 4096 8.1 us, 9.9 with two pieces
+  // a lane in half the waves, 11.6 with four. Many long rows: two (2048 x 14336 20.7
+  // us, 21.8 with one; normed 28.1 and 31.0).
+  const int64_t each = a.rows >= 1024 && pieces > 512 ? 2 : 1;
   int64_t waves = (pieces + 64 * each - 1) / (64 * each);
   waves = waves <= 1 ? 1 : waves <= 2 ? 2 : waves <= 4 ? 4 : waves <= 8 ? 8 : 16;
-  const bool hold2 = pieces <= 128 * waves;
+  const int64_t hold = (pieces + 64 * waves - 1) / (64 * waves);
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gamma);
-  const bool wide = (at & 15) == 0 && a.K % kPiece == 0 && a.ldx * (int64_t)sizeof(In) % 16 == 0;
+  const bool wide = (at & 15) == 0 && a.K % 8 == 0 && a.ldx * (int64_t)sizeof(In) % 16 == 0;
   const dim3 grid = rows_grid(a.rows), block((unsigned)(64 * waves));
 #define SHARQ_QUANT_INT8(W, H) \
   hipLaunchKernelGGL((quantize_int8_kernel<In, kNorm, W, H>), grid, block, 0, stream, a)
-  if (wide) {
-    if (hold2) SHARQ_QUANT_INT8(true, 2); else SHARQ_QUANT_INT8(true, kMost);
-  } else {
-    if (hold2) SHARQ_QUANT_INT8(false, 2); else SHARQ_QUANT_INT8(false, kMost);
-  }
+  if (!wide) SHARQ_QUANT_INT8(false, 2);
+  else if (hold <= 1) SHARQ_QUANT_INT8(true, 1);
+  else if (hold <= 2) SHARQ_QUANT_INT8(true, 2);
+  else SHARQ_QUANT_INT8(true, 4);
 #undef SHARQ_QUANT_INT8
   return hipGetLastError();
 }
@@ -354,7 +431,7 @@ hipError_t launch_rows(const QuantArgs& a, hipStream_t stream) {
 
 hipError_t launch_quantize_int8(const void* x, int dtype, int64_t E, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
                                 float* scales, const int32_t* seg, int32_t segments, hipStream_t stream) {
-  const QuantArgs a{x, ldx, nullptr, 0.0f, nullptr, (uint32_t)K, (uint32_t)(E * R), (uint32_t)R, codes, scales,
+  const QuantArgs a{x, ldx, nullptr, 0.0f, 0.0, nullptr, (uint32_t)K, (uint32_t)(E * R), (uint32_t)R, codes, scales,
                     seg, segments};
   if (dtype == 0) return launch_rows<float, false>(a, stream);
   if (dtype == 1) return launch_rows<uint16_t, false>(a, stream);
@@ -363,7 +440,7 @@ hipError_t launch_quantize_int8(const void* x, int dtype, int64_t E, int64_t R, 
 
 hipError_t launch_quantize_int8_rms(const uint16_t* x, int64_t T, int64_t K, int64_t ldx, const uint16_t* gamma,
                                     float eps, float* rms_scale, int8_t* codes, float* scales, hipStream_t stream) {
-  const QuantArgs a{x, ldx, gamma, eps, rms_scale, (uint32_t)K, (uint32_t)T, (uint32_t)T, codes, scales, nullptr, 0};
+  const QuantArgs a{x, ldx, gamma, eps, 1.0 / (double)K, rms_scale, (uint32_t)K, (uint32_t)T, (uint32_t)T, codes, scales, nullptr, 0};
   return launch_rows<uint16_t, true>(a, stream);
 }
 

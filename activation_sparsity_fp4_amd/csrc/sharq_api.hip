@@ -607,7 +607,7 @@ int sharq_linear_silu_int8(const int8_t* a_codes, const float* a_scales, const i
   if (rc != SHARQ_OK) return rc;
   const sharq::I8Product m{a_codes, a_scales, w_codes, w_scales, nullptr, T, 2 * I, K};
   if ((rc = check_i8(T, 2 * I, K)) != SHARQ_OK) return rc;
-  if (!sharq::i8_linear_fits(T, 2 * I + 64)) return SHARQ_EINVAL;  // 64: a partial last h tile
+  if (!sharq::i8_linear_fits(T, 2 * I)) return SHARQ_EINVAL;
   if (T == 0) return SHARQ_OK;
   if (i8_null(m)) return SHARQ_EINVAL;
   if ((rc = check_i8_h(T, I, h_codes, h_scales, workspace, workspace_bytes)) != SHARQ_OK) return rc;

@@ -142,7 +142,7 @@ hipError_t launch_quantize_int8_rms(const uint16_t* x, int64_t T, int64_t K, int
 hipError_t launch_pack_int8(const int8_t* codes_rm, int64_t E, int64_t R, int64_t K, int8_t* codes, bool unpack,
                             int8_t* out_rm, hipStream_t stream);
 
-// Products of 8-bit codes (i8gemm.hip): activation [ceil(K/64)][rows][64] against
+// Products of 8-bit codes (i8gemm.hip, i8grouped.hip): activation [ceil(K/64)][rows][64] against
 // weight [ceil(K/64)][O][64] (grouped: one such tensor per expert).
 struct I8Product {
   const int8_t* a_codes;

@@ -677,7 +677,7 @@ SHARQ_API int sharq_unpack_int8(const int8_t* codes, int64_t E, int64_t R, int64
  * The sum is exact; then one rounding to fp32, a product with sa and a fused one
  * with sw and the bias (a sum times sa past fp32's range is an infinity, whatever
  * sw). Codes and y 16-byte aligned, scales and bias 4.
- * Requires ceil(T / 64) * ceil(O / 64) < 2^22.
+ * Requires ceil(T / 256) * ceil(O / 256) < 2^22 (workgroups).
  */
 SHARQ_API int sharq_linear_int8(const int8_t* a_codes, const float* a_scales, const int8_t* w_codes,
                       const float* w_scales, const float* bias, int64_t T, int64_t O, int64_t K, void* y, int64_t ldy,
@@ -708,7 +708,7 @@ SHARQ_API int sharq_linear_silu_int8(const int8_t* a_codes, const float* a_scale
  *  workspace as above for (P, I).
  * Malformed segment or gather contents are handled as sharq_linear_grouped does
  * (a gathered row outside [0, T_src) counts as zeros). Requires
- * (P / 16 + min(P, E) + 1) * (O / 32 + 2) < 2^22 (workgroups).
+ * (P / 256 + min(P, E) + 1) * (O / 256 + 2) < 2^22 (workgroups).
  */
 SHARQ_API int sharq_linear_grouped_int8(const int8_t* a_codes, const float* a_scales, int64_t T_src,
                               const int32_t* a_rows, const int32_t* seg_offsets, int32_t E, const int8_t* w_codes,

@@ -58,7 +58,7 @@ def test_linear():
     assert linear(T=0, ac=0, y=0) == OK and linear(O=0) == OK
     for bad in (dict(T=-1), dict(O=-1), dict(K=0), dict(ldy=7), dict(dtype=2), dict(dtype=-1), dict(ac=0),
                 dict(asc=0), dict(wc=0), dict(ws=0), dict(y=0), dict(T=1 << 25), dict(O=1 << 25, ldy=1 << 25),
-                dict(T=1 << 20, O=1 << 20, ldy=1 << 20)):
+                dict(T=1 << 20, O=1 << 19, ldy=1 << 19)):
         assert linear(**bad) == EINVAL, bad
     assert linear(K=1 << 17) == ENOTIMPL
     for bad in (dict(ac=A + 8), dict(asc=B + 1), dict(wc=C + 4), dict(ws=D + 2), dict(bias=F + 1), dict(y=E_ + 4)):
@@ -77,7 +77,7 @@ def test_silu():
     assert silu(T=0, work=0, nbytes=0) == OK
     for bad in (dict(T=-1), dict(I=0), dict(I=-8), dict(K=0), dict(I=1 << 24), dict(ac=0), dict(ws=0), dict(hc=0),
                 dict(hs=0), dict(work=0, nbytes=0), dict(work=0), dict(nbytes=63), dict(nbytes=-1),
-                dict(T=1 << 20, I=1 << 16)):
+                dict(T=1 << 23, I=1 << 16)):
         assert silu(**bad) == EINVAL, bad
     assert silu(K=1 << 17) == ENOTIMPL and silu(I=1 << 17) == ENOTIMPL
     for bad in (dict(hc=E_ + 8), dict(hs=F + 2), dict(wc=C + 1), dict(work=G + 8)):
