@@ -95,7 +95,7 @@ struct I8Tile {
 // Named by rows x columns; kN: N groups divide K, where there are few tiles for the
 // chip; wide ones load fewer operand bytes a MFMA, narrow ones are more and finish
 // a stage sooner.
-using I8x64x64k4 = I8Tile<2, 2, 2, 2, 4, 4, 1>;
+using I8x64x64k2 = I8Tile<2, 2, 2, 2, 2, 4, 2>;
 using I8x64x128 = I8Tile<2, 4, 2, 2, 1, 4, 3>;
 using I8x64x128k2 = I8Tile<2, 4, 2, 2, 2, 6, 1>;
 using I8x128x128 = I8Tile<4, 4, 2, 2, 1, 3, 3>;
@@ -116,20 +116,23 @@ __device__ __forceinline__ int i8_swz(int row, int part) {
   return row * kRowBytes + ((part ^ i8_swz_part(row)) << 4);
 }
 
-// Weight rows behind the LDS rows of a tile, so that a lane's accumulators of
-// two (gate|up: four) neighbouring MFMA tiles are eight columns side by side:
+// Weight rows behind the LDS rows of a tile. A lane's accumulators of an MFMA tile
+// are four columns side by side, 16 bytes of fp32: LDS rows in order. For 16 bytes
+// of bf16 those of two (gate|up: four) neighbouring MFMA tiles are eight columns:
 // 32 LDS rows are 32 output columns, row 16 j + r column 8 (r / 4) + 4 j + r % 4;
 // gate|up: 64 rows are gate (j even) and up (j odd) of 32 h columns, row
 // 16 j + r h column 8 (r / 4) + 4 (j / 2) + r % 4 (with two MFMA tiles a wave 32
 // rows are gate and up of 16 h columns, in order).
-template <class C, bool kSilu>
+template <class C, int K>
 struct I8Cols {
   int64_t n0;  // first output (or h) column of the tile
   int64_t n;   // output (or h) columns
   static constexpr bool kEight = C::WN % 4 == 0;
   __device__ __forceinline__ int64_t w_row(int x) const {  // -1 past the last column
     const int j = x >> 4, r = x & 15;
-    if constexpr (!kSilu) {
+    if constexpr (K == kI8F32) {
+      return n0 + x < n ? n0 + x : -1;
+    } else if constexpr (K == kI8Bf16) {
       const int64_t o = n0 + 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
       return o < n ? o : -1;
     } else {
@@ -149,8 +152,8 @@ constexpr int kI8Cols = K == kI8Silu ? C::BN / 2 : C::BN;  // output (or h) colu
 // and threads between its MFMAs the reads of the next stage's and the loads of
 // stage s + ring into the slot that stage s left: at its barrier every wave has
 // stage s in registers, and stage s + 1 has landed.
-template <class C, bool kSilu>
-__device__ __forceinline__ void i8_mainloop(const I8Operands& op, const TileRows& tr, const I8Cols<C, kSilu>& tc,
+template <class C, int K>
+__device__ __forceinline__ void i8_mainloop(const I8Operands& op, const TileRows& tr, const I8Cols<C, K>& tc,
                                             uint8_t* lds, v4i (&acc)[C::WM][C::WN]) {
   const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kg = all / C::kGroup, wave = all % C::kGroup;
@@ -301,7 +304,9 @@ __device__ __forceinline__ void i8_store(Out* __restrict__ y, const float (&v)[k
   }
 }
 
-// The sum of a product's codes to its value: the int32 sum rounded once to fp32, a product and a fused one.
+// The sum of a product's codes to its value: the int32 sum rounded once to fp32, a
+// product and a fused one. (The gate and up values of a gate|up product are the same
+// without the bias's addition.)
 __device__ __forceinline__ float i8_value(int sum, float sa, float sw, float bias) {
   return fmaf((float)sum * sa, sw, bias);
 }
@@ -326,18 +331,19 @@ __device__ __forceinline__ void i8_epilogue(const v4i (&acc)[C::WM][C::WN], cons
     const float a = sa[row];
     Out* y = static_cast<Out*>(out.y) + (tr.m0 + row) * out.ld;
     if constexpr (K != kI8Silu) {
+      constexpr int kTiles = K == kI8F32 ? 1 : 2;
 #pragma unroll
-      for (int j = 0; j < C::WN; j += 2) {
-        float v[8];
+      for (int j = 0; j < C::WN; j += kTiles) {
+        float v[4 * kTiles];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kTiles; ++h) {
           const float4 w = four(C::kScaleW, j + h), b = four(C::kBias, j + h);
           v[4 * h] = i8_value(acc[i][j + h][0], a, w.x, b.x);
           v[4 * h + 1] = i8_value(acc[i][j + h][1], a, w.y, b.y);
           v[4 * h + 2] = i8_value(acc[i][j + h][2], a, w.z, b.z);
           v[4 * h + 3] = i8_value(acc[i][j + h][3], a, w.w, b.w);
         }
-        const int64_t o = n0 + 16 * (C::WN * wn + j) + 8 * lc;
+        const int64_t o = n0 + 16 * (C::WN * wn + j) + 4 * kTiles * lc;
         i8_store(y + o, v, o, n, out.wide);
       }
     } else {
@@ -351,8 +357,7 @@ __device__ __forceinline__ void i8_epilogue(const v4i (&acc)[C::WM][C::WN], cons
           const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            v[4 * h + r] = silu_times(i8_value(acc[i][j + 2 * h][r], a, gs[r], 0.0f),
-                                      i8_value(acc[i][j + 2 * h + 1][r], a, us[r], 0.0f));
+            v[4 * h + r] = silu_times((float)acc[i][j + 2 * h][r] * a * gs[r], (float)acc[i][j + 2 * h + 1][r] * a * us[r]);
         }
         const int64_t o = n0 + 8 * (C::WN * wn + j) + 4 * kPairs * lc;
         i8_store(y + o, v, o, n, out.wide);
@@ -373,10 +378,9 @@ __device__ __forceinline__ TileRows i8_dense_rows(int64_t m0, int64_t T, int bm)
 template <class C, int K>
 __device__ __forceinline__ void i8_tile(const I8Operands& op, const TileRows& tr, int64_t n0, const I8Out& out,
                                         uint8_t* lds) {
-  constexpr bool kSilu = K == kI8Silu;
-  const int64_t n = kSilu ? out.I : op.O;
+  const int64_t n = K == kI8Silu ? out.I : op.O;
   v4i acc[C::WM][C::WN];
-  i8_mainloop<C, kSilu>(op, tr, I8Cols<C, kSilu>{n0, n}, lds, acc);
+  i8_mainloop<C, K>(op, tr, I8Cols<C, K>{n0, n}, lds, acc);
   i8_epilogue<C, K>(acc, lds, tr, n0, n, out);
 }
 
@@ -443,21 +447,25 @@ __device__ __forceinline__ void i8_thin_tile(const I8Operands& op, const TileRow
     --left;
   };
   static_for<C::PF>(load);
-  // the scales of the columns that the thread finishes
-  const int unit = threadIdx.x;
+  // the scales of the columns that the thread finishes, four at a time
   constexpr int kCols = kSilu ? C::WN / 2 : C::WN, kUnits = 64 * C::WM * kCols;
-  static_assert(kUnits <= C::kThreads, "a thread finishes four columns at most");
-  const int ui = unit >> 6 < C::WM * kCols ? (unit >> 6) / kCols : 0, uj = (unit >> 6) % kCols;
-  float sa = 0.0f, sw[4], su[4], bias[4];
-  if (unit < kUnits) {
-    const int64_t src = tr.src(16 * ui + lr);
-    if (src >= 0) sa = op.a_scales[src];
+  constexpr int kEach = kUnits < C::kThreads ? 1 : kUnits / C::kThreads;
+  static_assert(kUnits < C::kThreads || kUnits % C::kThreads == 0, "threads finish columns alike");
+  float sa[kEach], sw[kEach][4], su[kEach][4], bias[kEach][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t o = w_row(kSilu ? 2 * uj : uj, 4 * lc + r);
-      sw[r] = o >= 0 ? op.w_scales[o] : 0.0f;
-      bias[r] = o >= 0 && op.bias ? op.bias[o] : 0.0f;
-      su[r] = kSilu && o >= 0 ? op.w_scales[o + n] : 0.0f;
+  for (int e = 0; e < kEach; ++e) {
+    const int unit = threadIdx.x + e * C::kThreads, i = (unit >> 6) / kCols, j = (unit >> 6) % kCols;
+    sa[e] = 0.0f;
+    if (unit < kUnits) {
+      const int64_t src = tr.src(16 * i + lr);
+      if (src >= 0) sa[e] = op.a_scales[src];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t o = w_row(kSilu ? 2 * j : j, 4 * lc + r);
+        sw[e][r] = o >= 0 ? op.w_scales[o] : 0.0f;
+        bias[e][r] = !kSilu && o >= 0 && op.bias ? op.bias[o] : 0.0f;
+        su[e][r] = kSilu && o >= 0 ? op.w_scales[o + n] : 0.0f;
+      }
     }
   }
   v4i acc[C::WM][C::WN];
@@ -483,27 +491,30 @@ __device__ __forceinline__ void i8_thin_tile(const I8Operands& op, const TileRow
 #pragma unroll
     for (int j = 0; j < C::WN; ++j) red[((wave * C::WM + i) * C::WN + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  if (unit >= kUnits) return;
-  auto sum = [&](int j) {
-    v4i v = v4i{};
 #pragma unroll
-    for (int q = 0; q < C::KW; ++q) v += red[((q * C::WM + ui) * C::WN + j) * 64 + lane];
-    return v;
-  };
-  float v[4];
-  if constexpr (kSilu) {
-    const v4i g = sum(2 * uj), u = sum(2 * uj + 1);
+  for (int e = 0; e < kEach; ++e) {
+    const int unit = threadIdx.x + e * C::kThreads, i = (unit >> 6) / kCols, j = (unit >> 6) % kCols, row = 16 * i + lr;
+    if (unit >= kUnits || row >= tr.rows_valid) continue;
+    auto sum = [&](int tile) {
+      v4i v = v4i{};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = silu_times(i8_value(g[r], sa, sw[r], 0.0f), i8_value(u[r], sa, su[r], 0.0f));
-  } else {
-    const v4i q = sum(uj);
+      for (int q = 0; q < C::KW; ++q) v += red[((q * C::WM + i) * C::WN + tile) * 64 + lane];
+      return v;
+    };
+    float v[4];
+    if constexpr (kSilu) {
+      const v4i g = sum(2 * j), u = sum(2 * j + 1);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = i8_value(q[r], sa, sw[r], bias[r]);
+      for (int r = 0; r < 4; ++r)
+        v[r] = silu_times((float)g[r] * sa[e] * sw[e][r], (float)u[r] * sa[e] * su[e][r]);
+    } else {
+      const v4i q = sum(j);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = i8_value(q[r], sa[e], sw[e][r], bias[e][r]);
+    }
+    const int64_t o = n0 + 16 * j + 4 * lc;
+    i8_store(static_cast<Out*>(out.y) + (tr.m0 + row) * out.ld + o, v, o, n, out.wide);
   }
-  const int row = 16 * ui + lr;
-  if (row >= tr.rows_valid) return;
-  const int64_t o = n0 + 16 * uj + 4 * lc;
-  i8_store(static_cast<Out*>(out.y) + (tr.m0 + row) * out.ld + o, v, o, n, out.wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -516,19 +527,19 @@ inline I8Operands i8_operands(const I8Product& p) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// For the choice of a tile alone, in microseconds: of a stage on the busiest CU,
-// by a workgroup's own chain and by each workgroup's share of the CU; of the ends
-// of each workgroup there; and of the launch.
+// For the choice of a tile alone, in microseconds: of a stage on a CU, by a
+// workgroup's own chain and by each workgroup's share of the CU; of the ends of each
+// workgroup there; and of the launch.
 struct I8TileCost {
   int64_t rows, cols;
   double chain, each, ends, launch;
+  int per_cu = 1;  // workgroups that share a CU
 };
 
-// `share` workgroups on the busiest CU, and no less than the bytes at the rate of memory.
-inline double i8_cost(const I8TileCost& c, double share, int64_t steps, double bytes) {
-  const double each = c.each * share;
-  const double loop = (double)steps * (c.chain > each ? c.chain : each) + c.ends * share, stream = bytes / 5.6e6;
-  return c.launch + (loop > stream ? loop + 0.1 * stream : stream + 0.1 * loop);
+// The loops of a launch, and no less than its bytes at the rate of memory.
+inline double i8_cost(double launch, double loops, double bytes) {
+  const double stream = bytes / 5.6e6;
+  return launch + (loops > stream ? loops + 0.1 * stream : stream + 0.1 * loops);
 }
 
 // Column tiles of a product of O weight rows (gate|up: of O / 2 h columns).

@@ -23,10 +23,17 @@ __global__ __launch_bounds__(C::kThreads) void i8_thin_kernel(I8Operands op, I8O
 
 constexpr int kI8Tiles = 12;
 constexpr I8TileCost kI8Costs[kI8Tiles] = {
-    {16, 32, 0.012, 0.040, 0.68, 2.6},   {32, 32, 0.051, 0.070, 0.57, 2.5},   {64, 32, 0.101, 0.067, 1.22, 3.2},
-    {64, 64, 0.056, 0.104, 1.18, 2.6},   {64, 128, 0.045, 0.180, 0.43, 2.2},  {64, 128, 0.055, 0.152, 0.98, 2.6},
-    {128, 128, 0.139, 0.230, 1.6, 3.0},  {128, 128, 0.125, 0.218, 1.18, 3.8}, {128, 256, 0.092, 0.477, 1.32, 2.75},
-    {256, 128, 0.106, 0.387, 1.16, 3.6}, {256, 128, 0.087, 0.325, 10.0, 0.0}, {256, 256, 0.110, 0.670, 2.7, 3.6}};
+    {16, 32, 0.014, 0.032, 1.96, 2.8, 4},   {32, 32, 0.007, 0.039, 1.28, 2.7, 4}, {64, 32, 0.001, 0.075, 2.74, 2.4, 2},
+    {64, 64, 0.045, 0.082, 1.31, 2.4, 2},   {64, 128, 0.042, 0.184, 1.57, 2.0, 3}, {64, 128, 0.152, 0.0, 1.82, 2.8},
+    {128, 128, 0.309, 0.197, 1.80, 2.1, 3}, {128, 128, 0.0, 0.197, 3.46, 2.2},     {128, 256, 0.278, 0.355, 4.9, 2.0, 2},
+    {256, 128, 0.464, 0.326, 3.26, 2.6, 2}, {256, 128, 0.0, 0.341, 5.46, 2.0},     {256, 256, 0.601, 0.0, 9.6, 2.8}};
+
+// n workgroups on the busiest CU: per_cu at a time, then the rest.
+double i8_loops(const I8TileCost& c, int64_t n, int64_t steps) {
+  auto stage = [&](int64_t together) { return c.each * (double)together > c.chain ? c.each * (double)together : c.chain; };
+  const int64_t rounds = n / c.per_cu, rest = n % c.per_cu;
+  return (double)steps * ((double)rounds * stage(c.per_cu) + (rest ? stage(rest) : 0.0)) + c.ends * (double)n;
+}
 
 // Calls f with the tile type of kI8Costs[tile] and whether it is a thin one.
 template <class F>
@@ -35,7 +42,7 @@ void i8_with_tile(int tile, F f) {
     case 0: f(I8Thin16{}, std::true_type{}); break;
     case 1: f(I8Thin32{}, std::true_type{}); break;
     case 2: f(I8Thin64{}, std::true_type{}); break;
-    case 3: f(I8x64x64k4{}, std::false_type{}); break;
+    case 3: f(I8x64x64k2{}, std::false_type{}); break;
     case 4: f(I8x64x128{}, std::false_type{}); break;
     case 5: f(I8x64x128k2{}, std::false_type{}); break;
     case 6: f(I8x128x128{}, std::false_type{}); break;
@@ -48,8 +55,13 @@ void i8_with_tile(int tile, F f) {
 }
 
 // The cheapest tile by the costs, which are fitted to timed launches of all of them
-// on 10 layer shapes from 512 x 4096 to 4096 x 28672 (K x O), T = 1 .. 4096, and
-// the 8192 x 57344 pair: within 1.3% of the best on average, 15% at most.
+// on 10 layer shapes from 512 x 4096 to 4096 x 28672 (K x O), T = 1 .. 4096, and on
+// larger ones at few tokens, the thin tiles favoured by 6% at up to 16 tokens (they
+// keep more of a cold weight in flight): within 1% of the best on average, 17% at
+// most. 1 x 28672 x 8192: 38 us in thin tiles, 75 to 220 in the others; 2048 x 4096 ->
+// 2 x 14336 193 us in 256 x 128, 200 in 128 x 256, 213 in 256 x 256; 256 x 4096 x 4096
+// 8.9 us in 64 x 64 with K in two, 12.2 in 64 x 128, 15 in 64 x 32; 2048 x 14336 x 4096
+// 95 us in 256 x 128 with K in two, 108 without.
 int i8_dense_tile(int64_t T, int64_t O, int64_t K, I8Kind kind) {
   const double bytes = ((double)O + (double)T) * (double)K + i8_out_bytes(T, O, kind);
   int pick = kI8Tiles - 1;
@@ -57,7 +69,8 @@ int i8_dense_tile(int64_t T, int64_t O, int64_t K, I8Kind kind) {
   for (int t = kI8Tiles - 1; t >= 0; --t) {
     const int64_t tiles = ceil_div(T, kI8Costs[t].rows) * i8_cols(O, kind == kI8Silu, kI8Costs[t]);
     if (tiles >= kI8MaxWorkgroups) break;  // narrower ones are more
-    const double us = i8_cost(kI8Costs[t], (double)ceil_div(tiles, 256), ceil_div(K, 64), bytes);
+    if ((t == 1 || t == 2) && T <= kI8Costs[t - 1].rows) continue;  // the thin tile of half the rows has them all
+    const double us = i8_cost(kI8Costs[t].launch, i8_loops(kI8Costs[t], ceil_div(tiles, 256), ceil_div(K, 64)), bytes);
     if (t == kI8Tiles - 1 || us < best) best = us, pick = t;
   }
   return pick;

@@ -16,7 +16,10 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_grouped_kern
     I8Operands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, int64_t P, I8Out out,
     int tiles_n) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
-  const GroupedTile g = grouped_tile<C, true>(seg, E, P, a_rows, op.rows, tiles_n);
+  // With column tiles in eights each XCD keeps a column slice of every weight, and all have the same work; otherwise
+  // an XCD takes a range of tiles, so that an expert's row tiles share its weight in one L2.
+  const GroupedTile g = (tiles_n & 7) == 0 ? grouped_tile<C, false>(seg, E, P, a_rows, op.rows, tiles_n)
+                                           : grouped_tile<C, true>(seg, E, P, a_rows, op.rows, tiles_n);
   if (g.e < 0) return;  // uniform across the workgroup
   i8_select_expert(op, g.e);
   // A tile with few rows (an expert's last) runs the loop of one of half or a quarter of the height: fewer MFMAs and
@@ -86,8 +89,10 @@ int i8_grouped_tile(int64_t P, int64_t E, int64_t O, int64_t K, I8Kind kind) {
     if (i8_grid(P, E, O, kind == kI8Silu, kI8Costs[t]) >= kI8MaxWorkgroups) break;  // narrower ones are more
     const double rows = mean / (double)kI8Costs[t].rows + 0.56;
     const double tiles = filled * (rows > 1 ? rows : 1) * (double)i8_cols(O, kind == kI8Silu, kI8Costs[t]);
-    const double us = i8_cost(kI8Costs[t], tiles > 256 ? tiles / 256 : 1, ceil_div(K, 64), bytes) +
-                      0.36 * tiles / 512;
+    const I8TileCost& c = kI8Costs[t];
+    const double share = tiles > 256 ? tiles / 256 : 1, each = c.each * share;
+    const double loops = (double)ceil_div(K, 64) * (c.chain > each ? c.chain : each) + c.ends * share;
+    const double us = i8_cost(c.launch, loops, bytes) + 0.36 * tiles / 512;
     if (t == kI8Tiles - 1 || us < best) best = us, pick = t;
   }
   return pick;
