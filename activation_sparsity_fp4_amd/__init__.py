@@ -929,7 +929,9 @@ class Int8(NamedTuple):
 def _int8_like(K, device, *rows):
     """An Int8 tensor of [.., R, K] for rows (.., R)."""
     torch = _torch()
-    return Int8(torch.empty((*rows[:-1], (K + 63) // 64, rows[-1], 64), dtype=torch.int8, device=device),
+    G = (K + 63) // 64
+    shape = (G, rows[0], 64) if len(rows) == 1 else (rows[0], G, rows[1], 64)
+    return Int8(torch.empty(shape, dtype=torch.int8, device=device),
                 torch.empty(rows, dtype=torch.float32, device=device), K)
 
 
@@ -938,11 +940,18 @@ def _check_int8(t, name, ndim=3):
     torch = _torch()
     codes, scales, K = t
     G = (K + 63) // 64
-    if type(codes) is type(scales) is torch.Tensor:
+    if type(codes) is type(scales) is torch.Tensor:  # the usual case, in as few steps as tell it
         shape = codes.shape
-        if (len(shape) == ndim and shape[-3] == G and shape[-1] == 64 and scales.shape == (*shape[:-3], shape[-2])
-                and codes.dtype is torch.int8 and scales.dtype is torch.float32 and codes.is_cuda and scales.is_cuda
-                and codes.is_contiguous() and scales.is_contiguous()):
+        if len(shape) == ndim == 3:
+            g, rows, width = shape
+            fits = scales.shape == (rows,)
+        elif len(shape) == ndim == 4:
+            experts, g, rows, width = shape
+            fits = scales.shape == (experts, rows)
+        else:
+            fits = False
+        if (fits and g == G and width == 64 and codes.dtype is torch.int8 and scales.dtype is torch.float32
+                and codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
             return shape
     _need(codes, torch.int8, name + ".codes", ndim)
     _need(scales, torch.float32, name + ".scales", ndim - 2)
@@ -977,30 +986,33 @@ def quantize_int8(x, out: Optional[Int8] = None, gamma=None, rms_eps: Optional[f
     torch = _torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if gamma is not None and rms_eps is None:
+    dtype = x.dtype
+    if rms_eps is not None:
+        _need(x, torch.bfloat16, "x", 2)  # the norm is for [R, K] activations
+        kind = 1
+    elif gamma is not None:
         raise ValueError("gamma is the weight of the norm: it needs rms_eps")
-    dtype = torch.bfloat16 if rms_eps is not None else x.dtype
-    kind = 0 if dtype == torch.float32 else 1 if dtype == torch.bfloat16 else 2 if dtype == torch.float16 else None
-    if kind is None:
-        raise TypeError(f"x must be float32, bfloat16 or float16, got {dtype}")
-    if x.dim() not in (2, 3):
+    else:
+        kind = 1 if dtype == torch.bfloat16 else 0 if dtype == torch.float32 else 2 if dtype == torch.float16 else None
+        if kind is None:
+            raise TypeError(f"x must be float32, bfloat16 or float16, got {dtype}")
+        if not x.is_cuda:
+            raise ValueError("x must be on the GPU")
+    shape = x.shape
+    if len(shape) == 2:
+        R, K = shape
+        E, ldx, rows = 1, x.stride(0) if R > 1 else K, (R,)
+    elif len(shape) == 3:
+        E, R, K = shape
+        ldx, rows = x.stride(1) if R > 1 else x.stride(0) if E > 1 else K, (E, R)
+        if E > 1 and R > 1 and x.stride(0) != R * ldx and (K == 1 or x.stride(2) == 1):
+            x, ldx = x.contiguous(), K
+    else:
         raise ValueError("x must have 2 or 3 dims")
-    if x.dim() == 3 and rms_eps is not None:
-        raise ValueError("the norm is for [R, K] activations")
-    _need(x, dtype, "x")
-    R, K = x.shape[-2:]
     if K < 1:
         raise ValueError("x must have at least one column")
-    if x.numel() and K > 1 and x.stride(-1) != 1:
+    if K > 1 and x.stride(-1) != 1 and x.numel():
         raise ValueError("x rows must be contiguous along K")
-    if x.dim() == 3:
-        E = x.shape[0]
-        ldx = x.stride(1) if R > 1 else x.stride(0) if E > 1 else K
-        if E > 1 and R > 1 and x.stride(0) != R * ldx:
-            x, ldx = x.contiguous(), K
-        rows = (E, R)
-    else:
-        E, ldx, rows = 1, _ld(x), (R,)
     out = _check_int8_out(out, K, x.device, *rows)
     if rms_eps is None:
         _same_device(x, out.codes, out.scales)

@@ -117,6 +117,12 @@ def check(fn: str, status: int) -> None:
         raise SharqError(fn, status)
 
 
+_entries = {}  # name -> function of the loaded library
+
+
 def call(name: str, *args) -> int:
     """Call an ABI entry point with raw integers (device addresses) and return its status."""
-    return getattr(lib(), name)(*args)
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(lib(), name)
+    return f(*args)
