@@ -16,8 +16,9 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_grouped_kern
     I8Operands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, int64_t P, I8Out out,
     int tiles_n) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
-  // With column tiles in eights each XCD keeps a column slice of every weight, and all have the same work; otherwise
-  // an XCD takes a range of tiles, so that an expert's row tiles share its weight in one L2.
+  // With column tiles in eights each XCD keeps a column slice of every weight, and all have the same work (1024 tokens x
+  // 2 of 8 experts, 4096 -> 2 x 14336: 280 us, 375 with ranges); otherwise an XCD takes a range of tiles, so that an
+  // expert's row tiles share its weight in one L2.
   const GroupedTile g = (tiles_n & 7) == 0 ? grouped_tile<C, false>(seg, E, P, a_rows, op.rows, tiles_n)
                                            : grouped_tile<C, true>(seg, E, P, a_rows, op.rows, tiles_n);
   if (g.e < 0) return;  // uniform across the workgroup
@@ -46,9 +47,9 @@ __global__ __launch_bounds__(C::kThreads) void i8_thin_grouped_kernel(I8Operands
 
 constexpr int kI8Tiles = 7;
 constexpr I8TileCost kI8Costs[kI8Tiles] = {
-    {16, 32, 0.072, 0.017, 1.59, 1.7},   {16, 64, 0.044, 0.032, 1.91, 2.6}, {64, 128, 0.057, 0.226, 0.44, 2.6},
-    {128, 128, 0.289, 0.262, 4.7, 2.3},  {128, 256, 1.07, 0.596, 1.86, 1.8}, {256, 128, 0.018, 0.353, 10.3, 3.4},
-    {256, 256, 0.096, 0.534, 10.5, 12.4}};
+    {16, 32, 0.094, 0.009, 1.16, 2.0},  {16, 64, 0.119, 0.028, 1.39, 2.4},  {64, 128, 0.012, 0.190, 0.61, 2.6},
+    {128, 128, 0.214, 0.286, 2.98, 2.1}, {128, 256, 0.603, 0.499, 2.18, 2.2}, {256, 128, 0.032, 0.338, 8.61, 3.5},
+    {256, 256, 0.554, 0.537, 9.11, 3.5}};
 
 // Calls f with the tile type of kI8Costs[tile] and whether it is a thin one.
 template <class F>
@@ -74,8 +75,8 @@ int64_t i8_grid(int64_t P, int64_t E, int64_t O, bool silu, const I8TileCost& c)
   return (i8_row_slots(P, E, c.rows) * i8_cols(O, silu, c) + 7) / 8 * 8;  // XCDs take equal shares
 }
 
-// The cheapest tile by the costs, for segments of about P / min(P, E) rows, 0.56 row
-// tiles more each for what does not fill one, and 0.36 us for every 512 workgroups'
+// The cheapest tile by the costs, for segments of about P / min(P, E) rows, 0.58 row
+// tiles more each for what does not fill one, and 0.42 us for every 512 workgroups'
 // lookup of their tile. Fitted to timed launches on 87 expert layers (8 to 128
 // experts, 2 to 32768 pairs), the thin tiles favoured by 6% at up to 4 rows an
 // expert (they keep more of a cold weight in flight): within 1% of the best on
@@ -87,12 +88,12 @@ int i8_grouped_tile(int64_t P, int64_t E, int64_t O, int64_t K, I8Kind kind) {
   double best = 0;
   for (int t = kI8Tiles - 1; t >= 0; --t) {
     if (i8_grid(P, E, O, kind == kI8Silu, kI8Costs[t]) >= kI8MaxWorkgroups) break;  // narrower ones are more
-    const double rows = mean / (double)kI8Costs[t].rows + 0.56;
+    const double rows = mean / (double)kI8Costs[t].rows + 0.58;
     const double tiles = filled * (rows > 1 ? rows : 1) * (double)i8_cols(O, kind == kI8Silu, kI8Costs[t]);
     const I8TileCost& c = kI8Costs[t];
     const double share = tiles > 256 ? tiles / 256 : 1, each = c.each * share;
     const double loops = (double)ceil_div(K, 64) * (c.chain > each ? c.chain : each) + c.ends * share;
-    const double us = i8_cost(c.launch, loops, bytes) + 0.36 * tiles / 512;
+    const double us = i8_cost(c.launch, loops, bytes) + 0.42 * tiles / 512;
     if (t == kI8Tiles - 1 || us < best) best = us, pick = t;
   }
   return pick;
