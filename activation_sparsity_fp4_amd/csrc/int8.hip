@@ -216,8 +216,9 @@ struct QuantArgs {
 // A workgroup has a row, a lane the pieces tid, tid + threads, ..., of which the
 // first kHold stay in registers between the passes over the row (a sum for the
 // norm, the maximum, the codes); later ones are read again. Many rows: bound by
-// memory where rows are long, by the instructions where they are short (an entry
-// takes about 8 of them, with the norm 16). Few: by one row's round trips.
+// memory (16384 x 4096 39 us, 5.2 TB/s, the rate of a copy), with the norm by its
+// instructions too (48 us). 2048 x 4096 8.1 us and 10.1, 4.9 at that rate: all rows are in
+// flight at once and wait together. Few: by one row's round trips (8 x 8192 3.6 and 4.5).
 template <class In, bool kNorm, bool kWide, int kHold>
 __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
   __shared__ double s_sum[16];

@@ -167,6 +167,16 @@ def test_quantize_strided(sq, R, K, ld, skip, kind):
     check_codes(sq.quantize_int8(t[:, skip:skip + k]), v[:, skip:skip + k])
 
 
+def test_quantize_more_rows_than_a_grid_is_wide(sq):
+    import torch
+    R, K = (1 << 20) + 5, 16
+    x = torch.randn((R, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    q = sq.quantize_int8(x)
+    rows = np.concatenate([np.arange(0, R, 9973), [(1 << 20) - 1, 1 << 20, R - 1]])
+    at = torch.from_numpy(rows).cuda()
+    check_codes(sq.Int8(q.codes[:, at], q.scales[at], K), x[at].float().cpu().numpy())
+
+
 def test_quantize_into_and_empty(sq):
     import torch
     v, t = typed(np.random.default_rng(0).standard_normal((9, 130)), "bf16")
@@ -444,6 +454,8 @@ GROUPED = [
     (4, 100, 200, [5, 20, 60, 60, 90], True),  # rows before the first segment
     (1, 130, 70, [0, 300], True),
     (8, 64, 1100, [300 * i for i in range(9)], True),
+    (6, 100, 2048, [0, 500, 500, 513, 900, 1700, 1710], True),  # column tiles in eights, row tiles of every height
+    (150, 64, 1024, [40 * i for i in range(151)], True),  # the same with more experts than two passes of a wave
 ]
 
 
