@@ -89,7 +89,7 @@ struct I8Tile {
   static constexpr int kWavesPerSimd = (WGS_ * kWaves + 3) / 4;
   static_assert(BN % 64 == 0 && WN % 2 == 0, "whole scale loads, columns in pairs");
   static_assert(kRing >= 3 && WGS_ * (kLds + 64) <= kLdsBytes, "ring");
-  // The same workgroup for half the rows (K undivided: an expert's last row tile).
+  // The same workgroup for half the rows: an expert's last row tile.
   using Half = I8Tile<(WM + 1) / 2, WN, NWM, NWN, KS, RING_, WGS_>;
 };
 // Named by rows x columns; kN: N groups divide K, where there are few tiles for the

@@ -646,3 +646,30 @@ def test_two_graphs_at_once(sq, T, K, I):
         assert same(eager, want[0])
         for i in range(2):
             assert all(same(y, want[i]) for y in outs[i]), (rep, i)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 8, 2, 96, 40), (60, 16, 4, 128, 64), (500, 5, 2, 128, 512)])
+def test_captured_expert_layer_with_new_inputs(sq, T, E, k, H, I):
+    """A captured expert layer, replayed on inputs and routings that change between the replays."""
+    import torch
+    xs, ls = [], []
+    for seed in range(4):
+        x, logits, gu, dn = _layer(sq, T, E, k, H, I, seed)
+        xs.append(bf16_to_gpu(x))
+        ls.append(f32_to_gpu(logits))
+    gu, dn = to_gpu(sq, *gu), to_gpu(sq, *dn)
+    counts = torch.tensor([[T], [T - 1], [T // 2], [0]], dtype=torch.int32, device="cuda")
+    want = [_run_layer(sq, xs[i], ls[i], k, gu, dn, counts[i])[-1] for i in range(4)]
+    x, logits, n = xs[0].clone(), ls[0].clone(), counts[0].clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = _run_layer(sq, x, logits, k, gu, dn, n)[-1]
+    for i in (0, 1, 2, 3, 0):
+        x.copy_(xs[i])
+        logits.copy_(ls[i])
+        n.copy_(counts[i])
+        out.fill_(float("nan"))
+        g.replay()
+        live = int(counts[i])
+        assert same(out[:live], want[i][:live]) and not out[live:].any()
