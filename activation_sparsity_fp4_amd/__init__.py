@@ -980,9 +980,10 @@ def quantize_int8(x, out: Optional[Int8] = None, gamma=None, rms_eps: Optional[f
     """8-bit codes of each row of x [R, K] (an activation [T, K], a weight [O, K])
     or of a stack of expert weights [E, O, K]: scale = amax / 127, codes rounded
     to nearest (ties to even). x is float32, bfloat16 or float16; rows may be
-    strided. A row that holds a NaN or an infinity has scale NaN and codes 0.
-    With rms_eps the rows of a bfloat16 [R, K] tensor are RMS-normed first
-    (per-row 1/rms, then gamma when given), as prepare(rms_eps=...) norms them."""
+    strided (unevenly spaced or overlapping ones are copied first). A row that
+    holds a NaN or an infinity has scale NaN and codes 0. With rms_eps the rows of
+    a bfloat16 [R, K] tensor are RMS-normed first (per-row 1/rms, then gamma when
+    given), as prepare(rms_eps=...) norms them."""
     torch = _torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
@@ -1005,14 +1006,15 @@ def quantize_int8(x, out: Optional[Int8] = None, gamma=None, rms_eps: Optional[f
     elif len(shape) == 3:
         E, R, K = shape
         ldx, rows = x.stride(1) if R > 1 else x.stride(0) if E > 1 else K, (E, R)
-        if E > 1 and R > 1 and x.stride(0) != R * ldx and (K == 1 or x.stride(2) == 1):
-            x, ldx = x.contiguous(), K
     else:
         raise ValueError("x must have 2 or 3 dims")
     if K < 1:
         raise ValueError("x must have at least one column")
     if K > 1 and x.stride(-1) != 1 and x.numel():
         raise ValueError("x rows must be contiguous along K")
+    # the library takes one distance of at least K between all rows; other tensors are copied
+    if ldx < K or (E > 1 and R > 1 and x.stride(0) != R * ldx):
+        x, ldx = x.contiguous(), K
     out = _check_int8_out(out, K, x.device, *rows)
     if rms_eps is None:
         _same_device(x, out.codes, out.scales)
