@@ -20,6 +20,7 @@ SHARQ_EHIP = -4
 SHARQ_ENOTIMPL = -5
 SHARQ_ESCRATCH = -6
 SCRATCHFREE_MAX_BYTES = 32 << 20  # SHARQ_SCRATCHFREE_MAX_BYTES
+ABI_VERSION = 10  # sharq_abi_version(): changes of what is there; additions are told by name
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -100,10 +101,16 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"{LIB_PATH} is missing: build it with `python -m activation_sparsity_fp4_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
+        rebuild = "rebuild it with `python -m activation_sparsity_fp4_amd.build`"
         for name, (res, args) in SIGNATURES.items():
-            fn = getattr(handle, name)
+            fn = getattr(handle, name, None)
+            if fn is None:
+                raise RuntimeError(f"{LIB_PATH} has no {name}, it was built from other sources: {rebuild}")
             fn.restype = res
             fn.argtypes = args
+        version = handle.sharq_abi_version()
+        if version != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} has ABI version {version}, not {ABI_VERSION}: {rebuild}")
         _lib = handle
     return _lib
 

@@ -85,7 +85,10 @@ enum { SHARQ_F32 = 0, SHARQ_BF16 = 1, SHARQ_F16 = 2 };
 /* Host. Static string describing a status code; never NULL. */
 SHARQ_API const char* sharq_status_string(int status);
 
-/* Host. Version of this ABI (bumped on any signature or layout change). */
+/*
+ * Host. Version of this ABI: raised by any change of a signature or a layout that
+ * was there. Entry points that are added leave it; a loader tells those by name.
+ */
 SHARQ_API int sharq_abi_version(void);
 
 /*
