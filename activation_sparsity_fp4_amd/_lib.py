@@ -80,6 +80,7 @@ SIGNATURES = {
                                          _P]),
     "sharq_linear_grouped_silu_int8": (_INT, [_P, _P, _I64, _P, _P, ctypes.c_int32, _P, _P, _I64, _I64, _I64, _P, _P,
                                               _P, _I64, _P]),
+    "sharq_int8_tile": (_INT, [_I64, ctypes.c_int32, _I64, _I64, _INT, _P]),
     "sharq_moe_combine_bf16": (_INT, [_P, _I64, _I64, _P, _P, _I64, ctypes.c_int32, _P, _P, _P]),
     "sharq_silu_mul": (_INT, [_P, _I64, _I64, _P, _P]),
 }

@@ -104,6 +104,11 @@ hipError_t i8_launch_dense(const I8Operands& op, const I8Out& out, int64_t K_, h
 
 }  // namespace
 
+I8TileChoice i8_linear_choice(int64_t T, int64_t O, int64_t K, int kind) {
+  const int tile = i8_dense_tile(T, O, K, (I8Kind)kind);
+  return I8TileChoice{tile, kI8Tiles, (int)kI8Costs[tile].rows, (int)kI8Costs[tile].cols};
+}
+
 bool i8_linear_fits(int64_t T, int64_t O) { return ceil_div(T, 256) * ceil_div(O, 256) < kI8MaxWorkgroups; }
 
 hipError_t launch_i8_linear(const I8Product& p, void* y, int64_t ldy, bool bf16, hipStream_t stream) {

@@ -129,6 +129,11 @@ hipError_t i8_launch_grouped(const I8Operands& op, const int32_t* a_rows, const 
 
 }  // namespace
 
+I8TileChoice i8_grouped_choice(int64_t P, int32_t E, int64_t O, int64_t K, int kind) {
+  const int tile = i8_grouped_tile(P, E, O, K, (I8Kind)kind);
+  return I8TileChoice{tile, kI8Tiles, (int)kI8Costs[tile].rows, (int)kI8Costs[tile].cols};
+}
+
 bool i8_grouped_fits(int64_t P, int32_t E, int64_t O) {
   return (i8_row_slots(P, E, 256) + 1) * (ceil_div(O, 256) + 1) < kI8MaxWorkgroups;
 }

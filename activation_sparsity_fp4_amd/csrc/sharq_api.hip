@@ -640,6 +640,19 @@ int sharq_linear_grouped_silu_int8(const int8_t* a_codes, const float* a_scales,
   return hip_status(sharq::launch_i8_grouped_silu(m, a_rows, seg_offsets, E, P, h_codes, h_scales, workspace, stream));
 }
 
+int sharq_int8_tile(int64_t rows, int32_t E, int64_t O, int64_t K, int kind, int32_t* tile) {
+  const int rc = check_i8(1, O, K);
+  if (rc != SHARQ_OK) return rc;
+  if (rows < 1 || O < 1 || E < 0 || kind < 0 || kind > 2 || (kind == 2 && O % 2) || !tile) return SHARQ_EINVAL;
+  if (E == 0 ? rows >= kMaxMxRows || !sharq::i8_linear_fits(rows, O)
+             : rows >= ((int64_t)1 << 31) || !sharq::i8_grouped_fits(rows, E, O))
+    return SHARQ_EINVAL;
+  const sharq::I8TileChoice c =
+      E == 0 ? sharq::i8_linear_choice(rows, O, K, kind) : sharq::i8_grouped_choice(rows, E, O, K, kind);
+  tile[0] = c.number, tile[1] = c.count, tile[2] = c.rows, tile[3] = c.cols;
+  return SHARQ_OK;
+}
+
 int64_t sharq_moe_route_workspace_bytes(int64_t T, int32_t E) {
   if (T < 0 || T >= ((int64_t)1 << 31) || E < 1 || E > 1024) return 0;
   return sharq::moe_route_workspace_bytes(T, E);

@@ -165,6 +165,14 @@ hipError_t launch_i8_grouped(const I8Product& p, const int32_t* a_rows, const in
 hipError_t launch_i8_grouped_silu(const I8Product& p, const int32_t* a_rows, const int32_t* seg, int32_t E, int64_t P,
                                   int8_t* h_codes, float* h_scales, void* workspace, hipStream_t stream);
 
+// The tile that a product runs on (kind: 0 fp32, 1 bf16, 2 gate|up; O: weight rows).
+struct I8TileChoice {
+  int number, count;  // of how many
+  int rows, cols;     // tokens, weight rows
+};
+I8TileChoice i8_linear_choice(int64_t T, int64_t O, int64_t K, int kind);
+I8TileChoice i8_grouped_choice(int64_t P, int32_t E, int64_t O, int64_t K, int kind);
+
 hipError_t launch_moe_combine_bf16(const uint16_t* y, int64_t P, int64_t H, const int32_t* pair_index,
                                    const float* weights, int64_t T, int k, float* out, uint16_t* out_bf16,
                                    hipStream_t stream);

@@ -723,6 +723,19 @@ SHARQ_API int sharq_linear_grouped_silu_int8(const int8_t* a_codes, const float*
                                    int8_t* h_codes, float* h_scales, void* workspace, int64_t workspace_bytes,
                                    hipStream_t stream);
 
+/*
+ * sharq_int8_tile -- Host. The tile that a product of 8-bit codes runs on, for tests
+ * and timings (results do not depend on it): the dense product of `rows` tokens with
+ * E = 0, the product per expert segment of `rows` pairs and E experts otherwise, of O
+ * weight rows (gate|up: 2 I). kind: SHARQ_F32 or SHARQ_BF16 results, or 2 for the
+ * gate|up product.
+ *  tile  i32 [4] (host): the tile's number, how many there are to choose from, its
+ *  tokens and its weight rows.
+ * SHARQ_EINVAL or SHARQ_ENOTIMPL where the product refuses the sizes, and for sizes
+ * without a result.
+ */
+SHARQ_API int sharq_int8_tile(int64_t rows, int32_t E, int64_t O, int64_t K, int kind, int32_t* tile);
+
 #ifdef __cplusplus
 }
 #endif
