@@ -21,8 +21,9 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_linear_kerne
   i8_tile<C, K>(op, i8_dense_rows((int64_t)ti.tm * C::BM, op.rows, C::BM), (int64_t)ti.tn * kI8Cols<C, K>, out, lds);
 }
 
-// Few tokens: bound by the weight's bytes (1 x 28672 x 8192 37.5 us, 6.2 TB/s; 8 x 8192 ->
-// 2 x 28672 81 us, 5.8 TB/s) or by the round trips of one (1 x 4096 x 4096 5.2 us).
+// Few tokens: bound by the weight's bytes (1 x 28672 x 8192 38 us, 6.2 TB/s; 8 x 8192 ->
+// 2 x 28672 83 us, 5.7 TB/s, where tiles through LDS take 82) or by the round trips of one
+// (1 x 4096 x 4096 5.2-5.6 us, 6.4 where the weight is in no cache).
 template <class C, int K>
 __global__ __launch_bounds__(C::kThreads) void i8_thin_kernel(I8Operands op, I8Out out, int tiles_m) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
@@ -63,14 +64,18 @@ void i8_with_tile(int tile, F f) {
   }
 }
 
-// The cheapest tile by the costs, which are fitted to timed launches of all of them
-// on 10 layer shapes from 512 x 4096 to 4096 x 28672 (K x O), T = 1 .. 4096, and on
-// larger ones at few tokens, the thin tiles favoured by 6% at up to 16 tokens (they
-// keep more of a cold weight in flight): within 1% of the best on average, 17% at
-// most. 1 x 28672 x 8192: 38 us in thin tiles, 75 to 220 in the others; 2048 x 4096 ->
-// 2 x 14336 193 us in 256 x 128, 200 in 128 x 256, 213 in 256 x 256; 256 x 4096 x 4096
-// 8.9 us in 64 x 64 with K in two, 12.2 in 64 x 128, 15 in 64 x 32; 2048 x 14336 x 4096
-// 95 us in 256 x 128 with K in two, 108 without.
+// The cheapest tile by the costs. They were fitted to launches of all tiles on 10 layer
+// shapes from 512 x 4096 to 4096 x 28672 (K x O), T = 1 .. 4096, and on larger ones at
+// few tokens; up to 16 tokens the fit took the other tiles' times 6% longer than they
+// were, for thin tiles keep more of a cold weight in flight: that preference is in the
+// constants. In graphs on cold weights the pick is 4% over the best on average at those
+// sizes, 11% at 64 held out (45% at most): the fit saw no launch below the 4.8 us that
+// the host takes for one, and products of less take 64 x 64 with K in two where 16 x 32
+// is shorter (1 x 768 x 2048 4.2 and 3.0 us). There also: 1 x 28672 x 8192 38-40 us in thin
+// tiles, 55 to 237 in the others; 2048 x 4096 -> 2 x 14336 192 us in 256 x 128, 198 in
+// 128 x 256, 216 in 256 x 256; 256 x 4096 x 4096 12.0 us in 64 x 64 with K in two, 17 in
+// 64 x 128, 18 in 64 x 32; 2048 x 14336 x 4096 96 us in 256 x 128 with K in two, 107
+// without.
 int i8_dense_tile(int64_t T, int64_t O, int64_t K, I8Kind kind) {
   const double bytes = ((double)O + (double)T) * (double)K + i8_out_bytes(T, O, kind);
   int pick = kI8Tiles - 1;

@@ -12,12 +12,13 @@ __device__ __forceinline__ void i8_select_expert(I8Operands& op, int e) {
 }
 
 // Per expert. Many tokens: bound by the ends of the workgroups' short loops and by cold
-// weights. 4096 tokens x 8 of 128 experts, 2048 -> 2 x 768 155-160 us, 768 -> 2048 102 us;
-// the same products dense 90 and 62, with segments of 256 rows each 141 and 90, with 64
-// experts of 512 rows 111 and 78. 1024 tokens x 2 of 8, 4096 -> 14336, ragged: 158 us for
-// 470 MB of weights (103 us) and tiles that fill 75% of their rows. (The experts' full row
-// tiles first and the short ones last: 171 us for 164 then; three quarters of the
-// height as a fourth loop: no gain.)
+// weights. 4096 tokens x 8 of 128 experts, 2048 -> 2 x 768 151-155 us (160-170 in the first
+// passes on new inputs), 768 -> 2048 98-105 us; the same products dense 90 and 62, with
+// segments of 256 rows each 141 and 90, with 64 experts of 512 rows 111 and 78. 1024 tokens
+// x 2 of 8, 4096 -> 14336, ragged: 157-160 us where the least is 103 (the 470 MB of weights
+// 91 of it), with tiles that fill 75% of their rows. (The experts' full row tiles first and
+// the short ones last: 171 us for 164 then; three quarters of the height as a fourth loop:
+// no gain.)
 template <class C, int K>
 __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_grouped_kernel(
     I8Operands op, const int32_t* __restrict__ a_rows, const int32_t* __restrict__ seg, int E, int64_t P, I8Out out,
@@ -25,7 +26,9 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void i8_grouped_kern
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
   // With column tiles in eights each XCD keeps a column slice of every weight, and all have the same work (1024 tokens x
   // 2 of 8 experts, 4096 -> 2 x 14336: 280 us, 375 with ranges); otherwise an XCD takes a range of tiles, so that an
-  // expert's row tiles share its weight in one L2.
+  // expert's row tiles share its weight in one L2. Column by column those widths take longer: there, of skewed segments,
+  // 10.4 us per 1000 weight rows at 14336 (112 column tiles), 12.9 at 11008 (86), 12.6 at 13824 (108); without SiLU
+  // 4096 -> 14336 11.1 (56), 11008 13.4 (43), 13824 12.1 (54).
   const GroupedTile g = (tiles_n & 7) == 0 ? grouped_tile<C, false>(seg, E, P, a_rows, op.rows, tiles_n)
                                            : grouped_tile<C, true>(seg, E, P, a_rows, op.rows, tiles_n);
   if (g.e < 0) return;  // uniform across the workgroup
@@ -87,10 +90,14 @@ int64_t i8_grid(int64_t P, int64_t E, int64_t O, bool silu, const I8TileCost& c)
 
 // The cheapest tile by the costs, for segments of about P / min(P, E) rows, 0.58 row
 // tiles more each for what does not fill one, and 0.42 us for every 512 workgroups'
-// lookup of their tile. Fitted to timed launches on 87 expert layers (8 to 128
-// experts, 2 to 32768 pairs), the thin tiles favoured by 6% at up to 4 rows an
-// expert (they keep more of a cold weight in flight): within 1% of the best on
-// average, 15% at most.
+// lookup of their tile. Fitted to timed launches on 88 expert layers (8 to 128
+// experts, 2 to 32768 pairs, even segments); up to 4 rows an expert the fit took the
+// other tiles' times 6% longer than they were, for thin tiles keep more of a cold
+// weight in flight: that preference is in the constants. In graphs on cold weights
+// the pick is 2.5% over the best on average there and 3.9% at 40 layers held out, with
+// skewed segments (24% at most). Farthest off: 16 to 32 rows each of 8 experts, 14336 ->
+// 4096, thin tiles where 64 x 128 is faster (128 x 2: 120 us for 79). The costs do not
+// know in which order of the column tiles a tile runs.
 int i8_grouped_tile(int64_t P, int64_t E, int64_t O, int64_t K, I8Kind kind) {
   const double filled = (double)(P < E ? P : E), mean = (double)P / filled;
   const double bytes = (filled * (double)O + (double)P) * (double)K + i8_out_bytes(P, O, kind);
