@@ -1,13 +1,14 @@
-// Pieces shared by the MXFP4 GEMMs (two-path and plain): the LDS swizzle, the
-// rows and columns behind an output tile, buffer loads into LDS and their
-// waits, the order of the tiles and the tile lookup of grouped launches.
+// Pieces shared by the GEMMs (two-path and plain MXFP4, 8-bit integer): the LDS
+// swizzle, the rows and columns behind an output tile, buffer loads into LDS and
+// their waits, the view of an operand's stage, the order of the tiles and the tile
+// lookup of grouped launches.
 #pragma once
 
 #include "sharq_device.h"
 
 namespace sharq {
 
-constexpr int kRowBytes = 64;            // 128 FP4 codes
+constexpr int kRowBytes = 64;            // 128 FP4 codes or 64 of a byte
 constexpr int kLdsBytes = 160 * 1024;    // LDS of one CU
 constexpr uint32_t kOOB = 0x80000000u;   // buffer offset past every bound: reads as 0
 

@@ -216,9 +216,12 @@ struct QuantArgs {
 // A workgroup has a row, a lane the pieces tid, tid + threads, ..., of which the
 // first kHold stay in registers between the passes over the row (a sum for the
 // norm, the maximum, the codes); later ones are read again. Many rows: bound by
-// memory (16384 x 4096 39 us, 5.2 TB/s, the rate of a copy), with the norm by its
-// instructions too (48 us). 2048 x 4096 8.1 us and 10.1, 4.9 at that rate: all rows are in
+// memory (16384 x 4096 39-45 us by card, 5.2-4.4 TB/s, the rate of a copy; of fp32 70 us,
+// 4.8 TB/s; weights 128 x 1536 x 2048 209 us, 5.8 TB/s), with the norm by its instructions
+// too (48-53 us). 2048 x 4096 8.1-8.6 us and 10.1-10.5, 4.9 at that rate: all rows are in
 // flight at once and wait together. Few: by one row's round trips (8 x 8192 3.6 and 4.5).
+// Rows that are not wide are read entry by entry: 16384 x 4097 145 us, of fp32 138, normed
+// 269.
 template <class In, bool kNorm, bool kWide, int kHold>
 __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
   __shared__ double s_sum[16];
@@ -351,7 +354,9 @@ __global__ __launch_bounds__(1024) void quantize_int8_kernel(QuantArgs a) {
   }
 }
 
-// Row-major codes [rows][K] to stages and back, a 16-byte piece of a stage a lane; kWide: rows are 16-byte aligned.
+// Row-major codes [rows][K] to stages and back, a 16-byte piece of a stage a lane; kWide: rows are 16-byte aligned. Bound
+// by memory then (14336 x 4096 24 us packed, 23 unpacked: 4.9-5.2 TB/s); others go byte by byte (14336 x 4100 98 and 140
+// us: a weight is packed once).
 template <bool kWide>
 __global__ __launch_bounds__(256) void pack_int8_kernel(const int8_t* __restrict__ rm, uint32_t per, uint32_t K,
                                                         int64_t chunks, int8_t* __restrict__ sm) {
