@@ -983,7 +983,8 @@ def quantize_int8(x, out: Optional[Int8] = None, gamma=None, rms_eps: Optional[f
     strided (unevenly spaced or overlapping ones are copied first). A row that
     holds a NaN or an infinity has scale NaN and codes 0. With rms_eps the rows of
     a bfloat16 [R, K] tensor are RMS-normed first (per-row 1/rms, then gamma when
-    given), as prepare(rms_eps=...) norms them."""
+    given), as prepare(rms_eps=...) norms them but for the order of the sum of
+    squares, which may change the last bit of 1/rms."""
     torch = _torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
@@ -1123,7 +1124,9 @@ def linear_grouped_int8(a: Int8, w: Int8, seg_offsets, a_rows=None, out=None, dt
     """linear_int8 per expert segment: row p of the [P, O] result (float32 or
     bfloat16) is activation row a_rows[p] (row p without a_rows) times the
     weight of the expert e with seg_offsets[e] <= p < seg_offsets[e + 1].
-    w.codes is [E, G, O, 64]. Rows of no segment are not written."""
+    w.codes is [E, G, O, 64]. Rows of no segment are not written. Rows of
+    bfloat16 are half the bytes for moe_combine to read, and are rounded once
+    more before it adds them up."""
     torch = _torch()
     T, E, O, P = _check_grouped_int8(a, w, seg_offsets, a_rows, "w")
     dtype, number = _out_dtype(out, dtype)
